@@ -16,6 +16,7 @@ DQ_CODEC_INT4, DQ_CODEC_E2M1, DQ_CODEC_E4M3, DQ_CODEC_E8M0, DQ_CODEC_BF16 = 0, 1
 DQ_CODEC_INT8 = 5
 DQ_NOALLOC_SCRATCH_BYTES = 4 << 20
 DQ_UPDATE_BOTH, DQ_UPDATE_ROW_ONLY, DQ_UPDATE_COL_ONLY = 0, 1, 2
+DQ_CACHE_BF16, DQ_CACHE_INT8 = 0, 1
 
 
 class dq_format(ctypes.Structure):
@@ -31,6 +32,26 @@ class dq_matrix(ctypes.Structure):
 
 class dq_solve_options(ctypes.Structure):
     _fields_ = [("update", c_int32), ("qchange", ctypes.POINTER(c_void_p))]
+
+
+class dq_kv_cache(ctypes.Structure):
+    _fields_ = [("kind", c_int32), ("page_size", c_int32), ("head_dim", c_int32),
+                ("kv_heads", c_int32), ("pages", c_int64), ("k", c_void_p), ("v", c_void_p),
+                ("page_stride", c_int64), ("head_stride", c_int64), ("row_stride", c_int64),
+                ("k_scales", c_void_p), ("v_scales", c_void_p)]
+
+
+class dq_rotary(ctypes.Structure):
+    _fields_ = [("cos", c_void_p), ("sin", c_void_p), ("positions", c_void_p),
+                ("rows", c_int64), ("dim", c_int32), ("interleaved", c_int32)]
+
+
+class dq_attention(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("out", c_void_p), ("q_stride", c_int64),
+                ("out_stride", c_int64), ("tokens", c_int64), ("sequences", c_int64),
+                ("heads", c_int32), ("causal", c_int32), ("q_starts", c_void_p),
+                ("lengths", c_void_p), ("page_table", c_void_p), ("table_stride", c_int64),
+                ("max_q", c_int64), ("max_len", c_int64), ("scale", ctypes.c_float)]
 
 
 # name -> (restype, argtypes); the same names as the C ABI
@@ -65,6 +86,22 @@ SIGNATURES = {
     "dq_w4a4_linear": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p,
                                  c_void_p, c_void_p, c_void_p, c_int64, dq_format, c_void_p,
                                  c_int64, c_void_p, c_size_t, c_void_p]),
+    "dq_row_quant": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p,
+                               c_void_p, c_void_p]),
+    "dq_w8a8_gemm_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "dq_w8a8_gemm": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_int64,
+                               c_void_p, c_int32, c_int64, c_void_p, c_size_t, c_void_p]),
+    "dq_w8a8_linear_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "dq_w8a8_linear": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p,
+                                 c_void_p, c_int64, c_void_p, c_int32, c_int64, c_void_p,
+                                 c_size_t, c_void_p]),
+    "dq_kv_append": (c_int32, [ctypes.POINTER(dq_kv_cache), c_int64, c_int32, c_void_p, c_int64,
+                               c_void_p, c_int64, c_void_p, ctypes.POINTER(dq_rotary), c_void_p,
+                               c_int64, c_int32, c_void_p, c_int64, c_void_p]),
+    "dq_paged_attention_workspace_bytes": (c_size_t, [ctypes.POINTER(dq_kv_cache),
+                                                      ctypes.POINTER(dq_attention)]),
+    "dq_paged_attention": (c_int32, [ctypes.POINTER(dq_kv_cache), ctypes.POINTER(dq_attention),
+                                     c_void_p, c_size_t, c_void_p]),
     "dq_encode": (c_int32, [c_void_p, c_int64, c_int32, c_void_p, c_void_p]),
     "dq_decode": (c_int32, [c_void_p, c_int64, c_int32, c_void_p, c_void_p]),
     "dq_last_device_error": (c_int32, [c_void_p]),

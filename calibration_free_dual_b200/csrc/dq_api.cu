@@ -68,6 +68,7 @@ thread_local int32_t t_ev_used = 0;
 }  // namespace
 
 namespace dq {
+bool error_word(unsigned** out) { return err_word_ptr(out) == DQ_OK; }
 void count_launches(int n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 void timing_before(cudaStream_t s) {
   if (t_ev_used < t_ev_cap) cudaEventRecord(static_cast<cudaEvent_t>(t_ev_start[t_ev_used]), s);

@@ -1,0 +1,534 @@
+// dq_attn.cu — attention of new tokens over a paged key/value cache: row tiles of 16.
+//
+// Rows are (token, query head) pairs that share a key head; a warp computes S = Q K^T for its 16 rows
+// and 16 cache rows at a time, keeps the running maximum and sum of each row (binary32, log2
+// units) and adds P V to the output in registers: one pass over the cache, no scores in memory. The
+// four warps of a CTA take groups of 16 cache rows in turn, each through its own ring of asynchronous
+// copies (no barrier in the loop), and merge at the end; long sequences are split over CTAs
+// (`chunk` cache rows each) whose partial results a second kernel joins. The bound is the cache's bytes.
+//
+// INT8 cache: codes become fp16 exactly (an exponent byte beside each code and one subtraction), the keys'
+// scales multiply the scores, the values' scales the weights before their rounding to fp16. The
+// weights are kept relative to a running power of two above the values' scales, so that fp16's range
+// holds them whatever the scales are.
+#include <algorithm>
+
+#include "dq_attn.cuh"
+#include "dq_internal.h"
+
+namespace dq {
+namespace {
+
+constexpr unsigned FULL = 0xFFFFFFFFu;
+constexpr int WARPS = 4, NT = WARPS * 32;
+constexpr int KG = 16;                            // cache rows of a group
+
+template <int D, bool INT8>
+struct Ring {
+  static constexpr int RB = D * (INT8 ? 1 : 2);   // bytes of a cache row
+  static constexpr int CPR = RB / 16;
+  static constexpr int SLOT = 2 * KG * RB + (INT8 ? 2 * KG * 4 : 0);
+  static constexpr int DEPTH = INT8 ? 4 : 3;
+  static constexpr int RING = WARPS * DEPTH * SLOT;
+  static constexpr int PITCH = D + 4;             // merge buffer, floats
+  static constexpr int MERGE = WARPS * 16 * PITCH * 4 + WARPS * 16 * 8;
+  static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+  static __device__ __forceinline__ int k_chunk(int row, int ch) {
+    if (!INT8) return row * CPR + (ch ^ (row & 7));
+    return row * CPR + (D == 128 ? ch ^ ((row & 1) << 2) : ch);
+  }
+  static __device__ __forceinline__ int v_chunk(int row, int ch) {
+    if (!INT8) return row * CPR + (ch ^ (row & 7));
+    return row * CPR + (ch ^ (D == 128 ? ((row >> 1) & 3) << 1 : ((row >> 1) & 1) << 1));
+  }
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+template <int D, bool INT8>
+__global__ void __launch_bounds__(NT)
+attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
+  using R = Ring<D, INT8>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rq = lane >> 2, c = lane & 3;         // fragment row and column group
+  const dq_attention& a = A.a;
+  const dq_kv_cache& C = A.cache;
+  const int G = C.kv_heads, group = A.group;
+  const int64_t idx = blockIdx.x;
+  const int split = (int)(idx % P.splits);
+  const int g = (int)(idx / P.splits % G);
+  const int64_t rt = idx / P.splits / G;
+  const int b = blockIdx.y;
+  const SeqBounds sq = seq_bounds(a, b);
+  if (sq.bad && idx == 0 && tid == 0) atomicOr(A.err_word, ERRBIT_BADARG);
+  const int64_t rows = (int64_t)sq.n * group, row0 = rt * 16;
+  if (row0 >= rows) return;
+  const int64_t kb = split * P.chunk;
+  if (split > 0 && kb >= sq.len) return;
+  const int64_t last = row0 + 15 < rows ? row0 + 15 : rows - 1;
+  int64_t ke = min64(sq.len, kb + P.chunk);
+  ke = min64(ke, visible(a, sq, (int)(last / group)));
+
+  // this thread's two rows: query pointer, visible cache rows
+  const __nv_bfloat16* qp[2];
+  int lim[2];
+  bool there[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t r = row0 + rq + 8 * i;
+    there[i] = r < rows;
+    const int64_t t = there[i] ? r / group : 0;
+    lim[i] = there[i] ? visible(a, sq, (int)t) : 0;
+    const int h = g * group + (int)(there[i] ? r % group : 0);
+    qp[i] = static_cast<const __nv_bfloat16*>(a.q) + (sq.start + t) * a.q_stride + (int64_t)h * D;
+  }
+  // rows that every row of the tile sees need no mask
+  const int64_t all_see = visible(a, sq, (int)(row0 / group));
+
+  // Q fragments. bf16: k-step s, pairs at 16 s + 2c and + 8. INT8: the k order within 64 channels is
+  // the one in which a thread reads 16 codes of a cache row at once (channel 64u + 16c + 4w + 0..3
+  // in step 4u + w).
+  constexpr int KS = D / 16;
+  uint32_t qf[KS][4];
+  float sc[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) sc[i] = a.scale * 1.4426950408889634f;
+  if constexpr (!INT8) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          qf[s][i + 2 * h] = there[i] ? __ldg(reinterpret_cast<const uint32_t*>(qp[i] + 16 * s + 8 * h + 2 * c)) : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t w[D / 64][8];
+      float mx = 0.0f;
+#pragma unroll
+      for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (there[i]) v = __ldg(reinterpret_cast<const uint4*>(qp[i] + 64 * u + 16 * c + 8 * h));
+          w[u][4 * h] = v.x; w[u][4 * h + 1] = v.y; w[u][4 * h + 2] = v.z; w[u][4 * h + 3] = v.w;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = bf16x2_to_f2(w[u][4 * h + j]);
+            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+      const float f = f16_row_factor(mx);
+      sc[i] /= f;
+#pragma unroll
+      for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+        for (int w4 = 0; w4 < 4; ++w4)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float2 x = bf16x2_to_f2(w[u][2 * w4 + h]);
+            qf[4 * u + w4][i + 2 * h] = pack2<true>(x.x * f, x.y * f);
+          }
+    }
+  }
+
+  // ---- ring of asynchronous copies
+  unsigned char* ring = smem + warp * R::DEPTH * R::SLOT;
+  const int groups = ke > kb ? (int)((ke - kb + KG - 1) / KG) : 0;
+  const int* table = a.page_table + b * a.table_stride;
+  const int psz = C.page_size;
+  auto page_of = [&](int gi) { return gi < groups ? __ldg(table + (kb + (int64_t)gi * KG) / psz) : 0; };
+  int next_page = page_of(warp);
+  int issued = warp, slot_w = 0;
+  auto issue = [&]() {
+    if (issued < groups) {
+      const int64_t key0 = kb + (int64_t)issued * KG;
+      int page = next_page;
+      int live = (int)min64(KG, sq.len - key0);          // rows past the length: zeros
+      if (page < 0 || page >= C.pages) {
+        if (lane == 0) atomicOr(A.err_word, ERRBIT_BADARG);
+        page = 0;
+        live = 0;
+      }
+      const int prow = (int)(key0 % psz);
+      const int64_t at = (int64_t)page * C.page_stride + (int64_t)g * C.head_stride + (int64_t)prow * C.row_stride;
+      const int64_t es = INT8 ? 1 : 2;
+      const uint32_t kd = smem_addr(ring + slot_w * R::SLOT), vd = kd + KG * R::RB;
+#pragma unroll
+      for (int i = 0; i < KG * R::CPR / 32; ++i) {
+        const int row = (i * 32 + lane) / R::CPR, ch = lane % R::CPR;
+        const int64_t off = (at + row * C.row_stride) * es + ch * 16;
+        const int bytes = row < live ? 16 : 0;
+        copy16(kd + R::k_chunk(row, ch) * 16, static_cast<const char*>(C.k) + (row < live ? off : 0), bytes);
+        copy16(vd + R::v_chunk(row, ch) * 16, static_cast<const char*>(C.v) + (row < live ? off : 0), bytes);
+      }
+      if (INT8 && lane < 8) {
+        const int part = lane & 3;                                   // four scales
+        const float* src = (lane < 4 ? C.k_scales : C.v_scales) + ((int64_t)page * G + g) * psz + prow + 4 * part;
+        const int bytes = 4 * max(0, min(4, live - 4 * part));
+        copy16(vd + KG * R::RB + lane * 16, bytes > 0 ? src : C.k_scales, bytes);
+      }
+      issued += WARPS;
+      next_page = page_of(issued);
+    }
+    slot_w = slot_w + 1 == R::DEPTH ? 0 : slot_w + 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < R::DEPTH - 1; ++i) issue();
+
+  constexpr int NTL = D / 8;
+  float o[NTL][4] = {};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  float vunit = 0x1p-100f;               // INT8: power of two above the values' scales so far
+  int slot_r = 0;
+  for (int gi = warp; gi < groups; gi += WARPS) {
+    issue();
+    asm volatile("cp.async.wait_group %0;" :: "n"(R::DEPTH - 1) : "memory");
+    __syncwarp();
+    const unsigned char* kp = ring + slot_r * R::SLOT;
+    const unsigned char* vp = kp + KG * R::RB;
+    slot_r = slot_r + 1 == R::DEPTH ? 0 : slot_r + 1;
+    // ---- S = Q K^T
+    float s[2][4] = {};
+    if constexpr (!INT8) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t kf[4];
+        ldsm4(kf, smem_addr(kp) + R::k_chunk((lane >> 4) * 8 + (lane & 7), 2 * ks + ((lane >> 3) & 1)) * 16);
+        mma16<false>(s[0], qf[ks], kf[0], kf[1]);
+        mma16<false>(s[1], qf[ks], kf[2], kf[3]);
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) {
+          const uint4 v = *reinterpret_cast<const uint4*>(kp + R::k_chunk(8 * t + rq, 4 * u + c) * 16);
+          const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma16<true>(s[t], qf[4 * u + i], codes_lo_f16(w[i]), codes_hi_f16(w[i]));
+        }
+    }
+    float vs[4];
+    if constexpr (INT8) {
+      const float2* scl = reinterpret_cast<const float2*>(vp + KG * R::RB);
+      const float2 k0 = scl[c], k1 = scl[4 + c], v0 = scl[8 + c], v1 = scl[12 + c];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        s[0][2 * i] *= k0.x; s[0][2 * i + 1] *= k0.y;
+        s[1][2 * i] *= k1.x; s[1][2 * i + 1] *= k1.y;
+      }
+      vs[0] = v0.x; vs[1] = v0.y; vs[2] = v1.x; vs[3] = v1.y;
+    }
+    // ---- mask, running maximum
+    const int64_t key0 = kb + (int64_t)gi * KG;
+    const bool mask = key0 + KG > all_see || key0 + KG > ke || row0 + 16 > rows;
+    float top[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float& x = s[t][2 * i + j];
+          x *= sc[i];
+          if (mask && key0 + 8 * t + 2 * c + j >= min64(lim[i], ke)) x = -INFINITY;
+        }
+      top[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+      top[i] = fmaxf(top[i], __shfl_xor_sync(FULL, top[i], 1));
+      top[i] = fmaxf(top[i], __shfl_xor_sync(FULL, top[i], 2));
+      top[i] = fmaxf(top[i], m[i]);
+    }
+    bool grow = top[0] > m[0] || top[1] > m[1];
+    float unit = vunit;
+    if constexpr (INT8) {
+      float vmax = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
+      vmax = fmaxf(vmax, __shfl_xor_sync(FULL, vmax, 1));
+      vmax = fmaxf(vmax, __shfl_xor_sync(FULL, vmax, 2));
+      if (vmax > vunit && vmax < 0x1p126f) unit = __uint_as_float((__float_as_uint(vmax) & 0x7F800000u) + 0x00800000u);
+      grow = grow || unit > vunit;
+    }
+    if (__any_sync(FULL, grow)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float al = top[i] == -INFINITY ? 1.0f : exp2_fast(m[i] - top[i]);
+        m[i] = top[i];
+        l[i] *= al;
+        const float ao = INT8 ? al * (vunit / unit) : al;
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) {
+          o[n][2 * i] *= ao;
+          o[n][2 * i + 1] *= ao;
+        }
+      }
+      vunit = unit;
+    }
+    // ---- P
+    uint32_t pf[4];
+    const float vinv = INT8 ? 0x1p15f / vunit : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float mm = m[i] == -INFINITY ? 0.0f : m[i];
+      float p[4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) p[2 * t + j] = exp2_fast(s[t][2 * i + j] - mm);
+      if constexpr (INT8) {
+        l[i] += (p[0] + p[1]) + (p[2] + p[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] *= vs[j] * vinv;
+        pf[i] = pack2<true>(p[0], p[1]);
+        pf[2 + i] = pack2<true>(p[2], p[3]);
+      } else {
+        // (the sum takes the weights before their rounding)
+        l[i] += (p[0] + p[1]) + (p[2] + p[3]);
+        pf[i] = pack2<false>(p[0], p[1]);
+        pf[2 + i] = pack2<false>(p[2], p[3]);
+      }
+    }
+    // ---- O += P V
+    if constexpr (!INT8) {
+#pragma unroll
+      for (int n = 0; n < NTL; n += 2) {
+        uint32_t vf[4];
+        ldsm4t(vf, smem_addr(vp) + R::v_chunk(((lane >> 3) & 1) * 8 + (lane & 7), n + (lane >> 4)) * 16);
+        mma16<false>(o[n], pf, vf[0], vf[1]);
+        mma16<false>(o[n + 1], pf, vf[2], vf[3]);
+      }
+    } else {
+      // rows 2c, 2c+1, 2c+8, 2c+9, D/8 codes each from channel (D/8) rq: column n of the product's
+      // tile e is channel (D/8) n + e
+      constexpr int W = D / 32;
+      uint32_t v[4][W];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = 2 * c + (k & 1) + 8 * (k >> 1);
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(vp + R::v_chunk(row, rq) * 16);
+          v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(vp + R::v_chunk(row, rq >> 1) * 16 + 8 * (rq & 1));
+          v[k][0] = x.x; v[k][1] = x.y;
+        }
+#pragma unroll
+        for (int w = 0; w < W; ++w) v[k][w] ^= 0x80808080u;
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+        const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140), b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+        mma16<true>(o[4 * w + 0], pf, codes_lo_f16(a0), codes_lo_f16(b0));
+        mma16<true>(o[4 * w + 1], pf, codes_hi_f16(a0), codes_hi_f16(b0));
+        mma16<true>(o[4 * w + 2], pf, codes_lo_f16(a1), codes_lo_f16(b1));
+        mma16<true>(o[4 * w + 3], pf, codes_hi_f16(a1), codes_hi_f16(b1));
+      }
+    }
+    __syncwarp();                        // the slot is free for the next copies
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  // ---- merge the warps: maxima and sums, then the outputs on one scale
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(FULL, l[i], 1);
+    l[i] += __shfl_xor_sync(FULL, l[i], 2);
+  }
+  __syncthreads();
+  float* mo = reinterpret_cast<float*>(smem);
+  float2* ml = reinterpret_cast<float2*>(smem + WARPS * 16 * R::PITCH * 4);
+  if (c == 0) {
+    ml[warp * 16 + rq] = make_float2(m[0], l[0]);
+    ml[warp * 16 + rq + 8] = make_float2(m[1], l[1]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, ml[w * 16 + rq + 8 * i].x);
+    float f = m[i] == -INFINITY ? 0.0f : exp2_fast(m[i] - mx);
+    if (INT8) f *= vunit * 0x1p-15f;
+    float* dst = mo + (warp * 16 + rq + 8 * i) * R::PITCH;
+    if constexpr (!INT8) {
+#pragma unroll
+      for (int n = 0; n < NTL; ++n)
+        *reinterpret_cast<float2*>(dst + 8 * n + 2 * c) = make_float2(o[n][2 * i] * f, o[n][2 * i + 1] * f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int n = 0; n < NTL; n += 4)
+          *reinterpret_cast<float4*>(dst + (D / 8) * (2 * c + j) + n) =
+              make_float4(o[n][2 * i + j] * f, o[n + 1][2 * i + j] * f, o[n + 2][2 * i + j] * f, o[n + 3][2 * i + j] * f);
+    }
+  }
+  __syncthreads();
+  // eight threads a row
+  const int r = tid / 8, e = tid % 8;
+  if (row0 + r >= rows) return;
+  float mx = -INFINITY, sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, ml[w * 16 + r].x);
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const float2 x = ml[w * 16 + r];
+    sum += x.x == -INFINITY ? 0.0f : x.y * exp2_fast(x.x - mx);
+  }
+  const int64_t t = sq.start + (row0 + r) / group;
+  const int h = g * group + (int)((row0 + r) % group);
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    const int d = 32 * j + 4 * e;
+    float4 x = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(mo + (w * 16 + r) * R::PITCH + d);
+      x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+    }
+    if (P.splits == 1) {
+      const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+      uint2 w;
+      w.x = pack2<false>(x.x * inv, x.y * inv);
+      w.y = pack2<false>(x.z * inv, x.w * inv);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + t * a.out_stride + (int64_t)h * D + d) = w;
+    } else {
+      const int64_t at = ((int64_t)split * a.tokens + t) * a.heads + h;
+      *reinterpret_cast<float4*>(P.part_o + at * D + d) = x;
+    }
+  }
+  if (P.splits > 1 && e == 0)
+    P.part_ml[((int64_t)split * a.tokens + t) * a.heads + h] = make_float2(mx, sum);
+}
+
+// Joins the splits: one warp per (token, head) row
+template <int D>
+__global__ void __launch_bounds__(128)
+attn_join_kernel(const AttnArgs A, const AttnPlan P) {
+  const dq_attention& a = A.a;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+  const int b = blockIdx.y;
+  const SeqBounds sq = seq_bounds(a, b);
+  const int64_t i = row / a.heads;
+  const int h = (int)(row % a.heads);
+  if (i >= sq.n) return;
+  const int splits = sq.len == 0 ? 1 : (int)((sq.len + P.chunk - 1) / P.chunk);
+  const int64_t at0 = (sq.start + i) * a.heads + h, pitch = a.tokens * a.heads;
+  float mx = -INFINITY;
+  for (int s = 0; s < splits; ++s) mx = fmaxf(mx, P.part_ml[s * pitch + at0].x);
+  float x[D / 32] = {}, sum = 0.0f;
+  for (int s = 0; s < splits; ++s) {
+    const float2 ml = P.part_ml[s * pitch + at0];
+    if (ml.x == -INFINITY) continue;
+    const float f = exp2_fast(ml.x - mx);
+    sum += ml.y * f;
+    const float* src = P.part_o + (s * pitch + at0) * D + lane * (D / 32);
+    if constexpr (D == 128) {
+      const float4 y = *reinterpret_cast<const float4*>(src);
+      x[0] += y.x * f; x[1] += y.y * f; x[2] += y.z * f; x[3] += y.w * f;
+    } else {
+      const float2 y = *reinterpret_cast<const float2*>(src);
+      x[0] += y.x * f; x[1] += y.y * f;
+    }
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (sq.start + i) * a.out_stride + (int64_t)h * D + lane * (D / 32);
+#pragma unroll
+  for (int j = 0; j < D / 32; j += 2)
+    *reinterpret_cast<uint32_t*>(dst + j) = pack2<false>(x[j] * inv, x[j + 1] * inv);
+}
+
+AttnPlan plan_attention(const AttnArgs& A, void* ws) {
+  AttnPlan P = {};
+  const dq_attention& a = A.a;
+  P.tile = 16;
+  P.row_tiles = (a.max_q * A.group + 15) / 16;
+  const int64_t base = P.row_tiles * A.cache.kv_heads * a.sequences;
+  // enough CTAs for every SM to hold two, none with less than 256 cache rows
+  const int64_t want = base > 0 ? (2 * SERVE_SMS + base - 1) / base : 1;
+  const int64_t most = std::max<int64_t>(1, a.max_len / 256);
+  P.splits = std::max<int64_t>(1, std::min(want, most));
+  P.chunk = std::max<int64_t>(64, ((a.max_len + P.splits - 1) / P.splits + 63) / 64 * 64);
+  P.splits = std::max<int64_t>(1, (a.max_len + P.chunk - 1) / P.chunk);
+  if (P.splits > 1 && ws != nullptr) {
+    const int64_t rows = P.splits * a.tokens * a.heads;
+    P.part_ml = static_cast<float2*>(ws);
+    P.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up((size_t)rows * 8, 256));
+  }
+  return P;
+}
+
+template <int D, bool INT8>
+cudaError_t launch_kind(const AttnArgs& A, const AttnPlan& P, cudaStream_t s) {
+  using R = Ring<D, INT8>;
+  constexpr auto K = attn_rows_kernel<D, INT8>;
+  cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, R::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t x = P.splits * A.cache.kv_heads * P.row_tiles;
+  if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
+  K<<<dim3((unsigned)x, (unsigned)A.a.sequences), NT, R::SMEM, s>>>(A, P);
+  count_launches(1);
+  if ((e = cudaGetLastError()) != cudaSuccess || P.splits == 1) return e;
+  const int64_t rows = A.a.max_q * A.a.heads;
+  attn_join_kernel<D><<<dim3((unsigned)((rows + 3) / 4), (unsigned)A.a.sequences), 128, 0, s>>>(A, P);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(const AttnArgs& A) {
+  const AttnPlan P = plan_attention(A, nullptr);
+  if (P.splits == 1) return 16;
+  const size_t rows = (size_t)P.splits * A.a.tokens * A.a.heads;
+  return align_up(rows * 8, 256) + rows * A.cache.head_dim * 4;
+}
+
+cudaError_t launch_attention(const AttnArgs& A, void* workspace, cudaStream_t s) {
+  const AttnPlan P = plan_attention(A, workspace);
+  const bool q8 = A.cache.kind == DQ_CACHE_INT8;
+  if (A.cache.head_dim == 64) return q8 ? launch_kind<64, true>(A, P, s) : launch_kind<64, false>(A, P, s);
+  return q8 ? launch_kind<128, true>(A, P, s) : launch_kind<128, false>(A, P, s);
+}
+
+}  // namespace dq

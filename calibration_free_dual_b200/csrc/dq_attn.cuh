@@ -1,0 +1,85 @@
+// dq_attn.cuh — what the paged attention kernels share: the plan of a call, a sequence's bounds, and
+// the conversions of INT8 cache codes.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "dq_device.cuh"
+#include "dq_serve.h"
+
+namespace dq {
+
+// How a call is split: `chunk` cache rows per CTA and `splits` of them per sequence, row tiles of
+// `tile` (token, head) rows of one key head
+struct AttnPlan {
+  int tile;
+  int64_t row_tiles, splits, chunk;
+  float* part_o;          // splits > 1: [splits][tokens * heads][head_dim] fp32, unnormalised
+  float2* part_ml;        // [splits][tokens * heads] (maximum, log2 units; sum)
+};
+
+namespace {
+
+__device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A sequence's new tokens and cache rows, clamped to the call's bounds; `bad` when they had to be
+struct SeqBounds {
+  int64_t start;
+  int n, len;
+  bool bad;
+};
+__device__ __forceinline__ SeqBounds seq_bounds(const dq_attention& a, int b) {
+  SeqBounds s;
+  int64_t lo = b, hi = b + 1;
+  if (a.q_starts != nullptr) {
+    lo = __ldg(a.q_starts + b);
+    hi = __ldg(a.q_starts + b + 1);
+  }
+  const int64_t len = __ldg(a.lengths + b);
+  s.bad = lo < 0 || hi < lo || hi > a.tokens || hi - lo > a.max_q || len < 0 || len > a.max_len;
+  lo = lo < 0 ? 0 : lo > a.tokens ? a.tokens : lo;
+  hi = hi < lo ? lo : hi > a.tokens ? a.tokens : hi;
+  s.start = lo;
+  s.n = (int)(hi - lo > a.max_q ? a.max_q : hi - lo);
+  s.len = (int)(len < 0 ? 0 : len > a.max_len ? a.max_len : len);
+  return s;
+}
+
+// cache rows that token i of n sees
+__device__ __forceinline__ int visible(const dq_attention& a, const SeqBounds& s, int i) {
+  if (!a.causal) return s.len;
+  const int v = s.len - s.n + i + 1;
+  return v < 0 ? 0 : v;
+}
+
+// Four INT8 codes (one word, already biased by xor 0x80808080) to fp16, exactly: a byte u under the
+// exponent of 1024 is 1024 + u, and u = code + 128. Pairs (0, 1) and (2, 3).
+__device__ __forceinline__ uint32_t sub_bias(uint32_t h2) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h2), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t codes_lo_f16(uint32_t u) {
+  return sub_bias(__byte_perm(u, 0x64646464u, 0x4140));
+}
+__device__ __forceinline__ uint32_t codes_hi_f16(uint32_t u) {
+  return sub_bias(__byte_perm(u, 0x64646464u, 0x4342));
+}
+
+// fp16 holds fewer powers of two than bf16, so a query row is scaled by a power of two before its
+// conversion: largest magnitude into [2^14, 2^15). A bf16 value keeps all its bits down to 2^-31 of
+// the row's largest.
+__device__ __forceinline__ float f16_row_factor(float absmax) {
+  int e = (int)(__float_as_uint(absmax) >> 23) - 127;
+  e = absmax > 0.0f ? (e < -100 ? -100 : e > 120 ? 120 : e) : 14;
+  return __uint_as_float((uint32_t)(14 - e + 127) << 23);
+}
+
+}  // namespace
+}  // namespace dq

@@ -1,0 +1,163 @@
+// dq_kv.cu — new tokens' keys and values into a paged cache, the keys (and the queries) rotated by
+// their positions on the way, in bf16 or as INT8 codes with one scale per (token, head).
+//
+// A memory-bound pass: every value is read once and written once. A head's row belongs to head_dim/8
+// threads, each with 8 channels in registers: with the half-split rotation four of the first
+// half and their four partners (no exchange between lanes), otherwise 8 in a row. A CTA takes one
+// token's rows of all heads, so the token's cos and sin are loaded once a thread. The INT8
+// row maximum is reduced by shuffles among the row's threads.
+#include <algorithm>
+
+#include "dq_device.cuh"
+#include "dq_internal.h"
+#include "dq_serve.h"
+
+namespace dq {
+namespace {
+
+constexpr unsigned FULL = 0xFFFFFFFFu;
+constexpr int KV_NT = 256;
+
+// four channels at `p`
+template <bool F32IN>
+__device__ __forceinline__ void load4(const char* p, float* x) {
+  if constexpr (F32IN) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);      // (q may be rotated in place)
+    const float2 a = bf16x2_to_f2(v.x), b = bf16x2_to_f2(v.y);
+    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+  }
+}
+
+__device__ __forceinline__ uint2 pack4(const float* x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+}
+
+template <int D, bool INT8, bool F32IN>
+__global__ void __launch_bounds__(KV_NT)
+kv_append_kernel(const AppendArgs A) {
+  constexpr int TPR = D / 8;                        // threads of one head's row
+  constexpr int RPP = KV_NT / TPR;                  // rows at a time
+  constexpr int ES = F32IN ? 4 : 2;
+  const int64_t t = blockIdx.x;
+  const int sub = threadIdx.x % TPR;
+  const dq_kv_cache& C = A.cache;
+  const int G = C.kv_heads, rows = A.q_heads + 2 * G;
+  const int64_t slot = __ldg(A.slots + t);
+  int64_t pos = 0;
+  bool ok = slot < C.pages * C.page_size;
+  if (A.rot.dim > 0) {
+    pos = __ldg(A.rot.positions + t);
+    ok = ok && pos >= 0 && pos < A.rot.rows;
+  }
+  if (!ok) {
+    if (threadIdx.x == 0) atomicOr(A.err_word, ERRBIT_BADARG);
+    return;
+  }
+  // this thread's channels lo..lo+3 and hi..hi+3 of a rotated row
+  const bool halves = A.rot.dim > 0 && !A.rot.interleaved;
+  const bool turned = 8 * sub < A.rot.dim;
+  const int lo_r = halves && turned ? 4 * sub : 8 * sub;
+  const int hi_r = halves && turned ? A.rot.dim / 2 + 4 * sub : 8 * sub + 4;
+  float cs[4] = {}, sn[4] = {};
+  if (turned) {
+    load4<true>(reinterpret_cast<const char*>(A.rot.cos + pos * (A.rot.dim / 2) + 4 * sub), cs);
+    load4<true>(reinterpret_cast<const char*>(A.rot.sin + pos * (A.rot.dim / 2) + 4 * sub), sn);
+  }
+  const int64_t page = slot < 0 ? 0 : slot / C.page_size, prow = slot < 0 ? 0 : slot % C.page_size;
+  bool bad = false;
+  // rows of the token: keys, values, queries (whole warps run the same count of rounds)
+  for (int r0 = 0; r0 < rows; r0 += RPP) {
+    const int r = r0 + threadIdx.x / TPR;
+    const bool is_q = r >= 2 * G, is_v = !is_q && r >= G;
+    const bool live = r < rows && (is_q || slot >= 0);
+    const int h = is_q ? r - 2 * G : is_v ? r - G : r;
+    const int lo = is_v ? 8 * sub : lo_r, hi = is_v ? 8 * sub + 4 : hi_r;
+    float x[8] = {};
+    if (live) {
+      const char* src = is_q ? static_cast<const char*>(A.q) + (t * A.q_stride + (int64_t)h * D) * ES
+                        : is_v ? static_cast<const char*>(A.v) + (t * A.v_stride + (int64_t)h * D) * ES
+                               : static_cast<const char*>(A.k) + (t * A.k_stride + (int64_t)h * D) * ES;
+      load4<F32IN>(src + lo * ES, x);
+      load4<F32IN>(src + hi * ES, x + 4);
+      if (!is_v && turned) {
+        if (halves) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) turn(x[i], x[4 + i], cs[i], sn[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
+        }
+      }
+    }
+    const int64_t at = page * C.page_stride + (int64_t)h * C.head_stride + prow * C.row_stride;
+    if (INT8) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+      for (int off = 1; off < TPR; off <<= 1) a = max(a, __shfl_xor_sync(FULL, a, off));
+      if (live && !is_q) {
+        const bool inf = a >= 0x7F800000u;
+        float d = fmaxf(div_qmax<127>(__uint_as_float(a)), 0x1p-126f), inv = __frcp_rn(d);
+        if (a == 0u) d = inv = 0.0f;
+        if (inf) {
+          d = __uint_as_float(0x7FC00000u);
+          inv = 0.0f;
+          bad = true;
+        }
+        // (rounding as in the row quantizer: no code leaves -127..127)
+        uint32_t b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          b[i] = __float_as_uint(__fadd_rn(__fmul_rn(x[i], inv), 12582912.0f));
+        uint32_t w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        uint32_t w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+        if (inf) w0 = w1 = 0u;
+        int8_t* dst = static_cast<int8_t*>(is_v ? C.v : C.k) + at;
+        *reinterpret_cast<uint32_t*>(dst + lo) = w0;
+        *reinterpret_cast<uint32_t*>(dst + hi) = w1;
+        if (sub == 0) (is_v ? C.v_scales : C.k_scales)[(page * G + h) * C.page_size + prow] = d;
+        continue;
+      }
+    }
+    if (live) {
+      char* dst = is_q ? static_cast<char*>(A.q_out) + (t * A.q_out_stride + (int64_t)h * D) * 2
+                       : static_cast<char*>(is_v ? C.v : C.k) + at * 2;
+      *reinterpret_cast<uint2*>(dst + lo * 2) = pack4(x);
+      *reinterpret_cast<uint2*>(dst + hi * 2) = pack4(x + 4);
+    }
+  }
+  if (bad) atomicOr(A.err_word, ERRBIT_NONFINITE);
+}
+
+template <int D>
+cudaError_t launch_dim(const AppendArgs& A, int esize, cudaStream_t s) {
+  const unsigned g = (unsigned)A.tokens;
+  if (A.cache.kind == DQ_CACHE_INT8) {
+    if (esize == 4) kv_append_kernel<D, true, true><<<g, KV_NT, 0, s>>>(A);
+    else kv_append_kernel<D, true, false><<<g, KV_NT, 0, s>>>(A);
+  } else {
+    if (esize == 4) kv_append_kernel<D, false, true><<<g, KV_NT, 0, s>>>(A);
+    else kv_append_kernel<D, false, false><<<g, KV_NT, 0, s>>>(A);
+  }
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendArgs& A, int esize, cudaStream_t s) {
+  return A.cache.head_dim == 64 ? launch_dim<64>(A, esize, s) : launch_dim<128>(A, esize, s);
+}
+
+}  // namespace dq

@@ -1,0 +1,249 @@
+// dq_serve_api.cu — the extern "C" entry points of the 8-bit serving path declared in include/dq.h:
+// argument checks (before anything is queued), workspace carving and launches. No allocation.
+#include <cmath>
+#include <cstdint>
+
+#include "dq.h"
+#include "dq_internal.h"
+#include "dq_serve.h"
+
+namespace {
+
+constexpr int64_t MAX_DIM = (int64_t)1 << 30;
+constexpr int64_t MAX_K8 = 131072;          // 127 * 127 * K < 2^31
+
+int esize_of(int32_t dt) { return dt == DQ_F32 ? 4 : (dt == DQ_BF16 ? 2 : 0); }
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+dq_status status_of(cudaError_t e) { return e == cudaSuccess ? DQ_OK : DQ_ERR_CUDA; }
+
+dq_status check_gemm8(int64_t T, int64_t N, int64_t K, const int8_t* w, const float* ws,
+                      const void* y, int32_t y_dtype, int64_t ldy) {
+  if (esize_of(y_dtype) == 0) return DQ_ERR_DTYPE;
+  if (T < 0 || N <= 0 || K <= 0 || ldy < N) return DQ_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K > MAX_K8 || T > MAX_DIM || N > MAX_DIM) return DQ_ERR_SHAPE;
+  if (T == 0) return DQ_OK;
+  if (w == nullptr || ws == nullptr || y == nullptr) return DQ_ERR_INVALID_ARG;
+  if (!aligned(w, 16) || !aligned(ws, 4) || !aligned(y, esize_of(y_dtype)))
+    return DQ_ERR_INVALID_ARG;
+  return DQ_OK;
+}
+
+// workspace of the linear layer: [scales | codes | the product's own]
+struct Linear8Ws {
+  size_t codes, gemm, total;
+};
+Linear8Ws linear8_ws(int64_t T, int64_t N, int64_t K) {
+  Linear8Ws l;
+  l.codes = dq::align_up((size_t)T * 4, 256);
+  l.gemm = l.codes + dq::align_up((size_t)T * (size_t)K, 256);
+  l.total = l.gemm + dq::gemm8_workspace_bytes(T, N, K);
+  return l;
+}
+
+dq_status check_cache(const dq_kv_cache* c, bool pointers) {
+  if (c == nullptr) return DQ_ERR_INVALID_ARG;
+  if (c->kind != DQ_CACHE_BF16 && c->kind != DQ_CACHE_INT8) return DQ_ERR_DTYPE;
+  if (c->head_dim != 64 && c->head_dim != 128) return DQ_ERR_UNSUPPORTED;
+  switch (c->page_size) {
+    case 16: case 32: case 64: case 128: case 256: break;
+    default: return DQ_ERR_UNSUPPORTED;
+  }
+  if (c->kv_heads <= 0 || c->kv_heads > 65535 || c->pages <= 0 || c->pages > INT32_MAX / 256)
+    return DQ_ERR_INVALID_ARG;
+  if (!pointers) return DQ_OK;
+  if (c->k == nullptr || c->v == nullptr || !aligned(c->k, 16) || !aligned(c->v, 16))
+    return DQ_ERR_INVALID_ARG;
+  const int64_t unit = c->kind == DQ_CACHE_BF16 ? 8 : 16;      // elements of 16 bytes
+  const int64_t lim = (int64_t)1 << 38;                        // a tensor map's stride limit
+  if (c->row_stride < c->head_dim || c->page_stride <= 0 || c->head_stride <= 0 ||
+      c->row_stride % unit || c->page_stride % unit || c->head_stride % unit ||
+      c->row_stride >= lim || c->page_stride >= lim || c->head_stride >= lim)
+    return DQ_ERR_INVALID_ARG;
+  if (c->kind == DQ_CACHE_INT8 &&
+      (c->k_scales == nullptr || c->v_scales == nullptr || !aligned(c->k_scales, 16) ||
+       !aligned(c->v_scales, 16)))
+    return DQ_ERR_INVALID_ARG;
+  return DQ_OK;
+}
+
+// sizes only; `group` receives the query heads per key head
+dq_status check_attention(const dq_kv_cache* c, const dq_attention* a, int* group) {
+  const dq_status st = check_cache(c, false);
+  if (st != DQ_OK) return st;
+  if (a == nullptr || a->tokens < 0 || a->sequences < 0 || a->heads <= 0 || a->max_q < 0 ||
+      a->max_len < 0)
+    return DQ_ERR_INVALID_ARG;
+  if (a->heads % c->kv_heads != 0) return DQ_ERR_SHAPE;
+  *group = a->heads / c->kv_heads;
+  if (*group > 128) return DQ_ERR_UNSUPPORTED;
+  if (a->tokens > INT32_MAX / 2 || a->sequences > 65535 || a->max_len > INT32_MAX / 2 ||
+      a->max_q > a->tokens)
+    return DQ_ERR_SHAPE;
+  return DQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dq_status dq_row_quant(const void* X, int32_t dtype, int64_t rows, int64_t n, int64_t ldx,
+                       const float* c, int8_t* codes, float* scales, void* stream) {
+  const int esize = esize_of(dtype);
+  if (esize == 0) return DQ_ERR_DTYPE;
+  if (rows < 0 || n <= 0 || ldx < n) return DQ_ERR_INVALID_ARG;
+  if (n % 16 != 0 || rows > MAX_DIM || n > MAX_DIM) return DQ_ERR_SHAPE;
+  if (rows == 0) return DQ_OK;
+  if (X == nullptr || codes == nullptr || scales == nullptr) return DQ_ERR_INVALID_ARG;
+  if (!aligned(X, 16) || (ldx * esize) % 16 != 0 || !aligned(c, 16) || !aligned(codes, 16) ||
+      !aligned(scales, 4))
+    return DQ_ERR_INVALID_ARG;
+  dq::RowsArgs A = {X, rows, n, ldx, c, codes, scales, nullptr};
+  if (!dq::error_word(&A.err_word)) return DQ_ERR_CUDA;
+  return status_of(dq::launch_row_quant(A, esize, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dq_w8a8_gemm_workspace_bytes(int64_t T, int64_t N, int64_t K) {
+  if (T < 0 || N <= 0 || K <= 0 || K % 16 != 0 || K > MAX_K8 || T > MAX_DIM || N > MAX_DIM)
+    return 0;
+  return dq::gemm8_workspace_bytes(T, N, K);
+}
+
+dq_status dq_w8a8_gemm(const int8_t* x, const float* x_scales, int64_t T, const int8_t* w,
+                       const float* w_scales, int64_t N, int64_t K, void* y, int32_t y_dtype,
+                       int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  const dq_status st = check_gemm8(T, N, K, w, w_scales, y, y_dtype, ldy);
+  if (st != DQ_OK || T == 0) return st;
+  if (x == nullptr || x_scales == nullptr || !aligned(x, 16) || !aligned(x_scales, 4))
+    return DQ_ERR_INVALID_ARG;
+  if (workspace == nullptr || workspace_bytes < dq_w8a8_gemm_workspace_bytes(T, N, K))
+    return DQ_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return DQ_ERR_INVALID_ARG;
+  dq::Gemm8Args A = {x, x_scales, w, w_scales, y, T, N, K, ldy, y_dtype == DQ_BF16, nullptr, 0};
+  if (!dq::error_word(&A.err_word)) return DQ_ERR_CUDA;
+  return status_of(dq::launch_gemm8(A, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dq_w8a8_linear_workspace_bytes(int64_t T, int64_t N, int64_t K) {
+  if (dq_w8a8_gemm_workspace_bytes(T, N, K) == 0) return 0;
+  return linear8_ws(T, N, K).total;
+}
+
+dq_status dq_w8a8_linear(const void* X, int32_t dtype, int64_t T, int64_t K, int64_t ldx,
+                         const float* c, const int8_t* w, const float* w_scales, int64_t N,
+                         void* y, int32_t y_dtype, int64_t ldy, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  const int esize = esize_of(dtype);
+  if (esize == 0) return DQ_ERR_DTYPE;
+  const dq_status st = check_gemm8(T, N, K, w, w_scales, y, y_dtype, ldy);
+  if (st != DQ_OK) return st;
+  if (ldx < K) return DQ_ERR_INVALID_ARG;
+  if (T == 0) return DQ_OK;
+  if (X == nullptr || !aligned(X, 16) || (ldx * esize) % 16 != 0 || !aligned(c, 16))
+    return DQ_ERR_INVALID_ARG;
+  const Linear8Ws l = linear8_ws(T, N, K);
+  if (workspace == nullptr || workspace_bytes < l.total) return DQ_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return DQ_ERR_INVALID_ARG;
+  char* ws = static_cast<char*>(workspace);
+  float* xs = reinterpret_cast<float*>(ws);
+  int8_t* codes = reinterpret_cast<int8_t*>(ws + l.codes);
+  unsigned* errp = nullptr;
+  if (!dq::error_word(&errp)) return DQ_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  dq::RowsArgs R = {X, T, K, ldx, c, codes, xs, errp};
+  const cudaError_t e = dq::launch_row_quant(R, esize, s);
+  if (e != cudaSuccess) return status_of(e);
+  dq::Gemm8Args A = {codes, xs, w, w_scales, y, T, N, K, ldy, y_dtype == DQ_BF16, errp, 1};
+  return status_of(dq::launch_gemm8(A, ws + l.gemm, s));
+}
+
+dq_status dq_kv_append(const dq_kv_cache* cache, int64_t tokens, int32_t dtype, const void* k,
+                       int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slots,
+                       const dq_rotary* rot, const void* q, int64_t q_stride, int32_t q_heads,
+                       void* q_out, int64_t q_out_stride, void* stream) {
+  const int esize = esize_of(dtype);
+  if (esize == 0) return DQ_ERR_DTYPE;
+  const dq_status st = check_cache(cache, true);
+  if (st != DQ_OK) return st;
+  if (tokens < 0) return DQ_ERR_INVALID_ARG;
+  if (tokens > MAX_DIM) return DQ_ERR_SHAPE;
+  const int64_t D = cache->head_dim, kv = cache->kv_heads * D;
+  const int64_t unit = 16 / esize;
+  if (k_stride < kv || v_stride < kv || k_stride % unit || v_stride % unit)
+    return DQ_ERR_INVALID_ARG;
+  if (rot != nullptr) {
+    if (rot->dim <= 0 || rot->dim % 8 != 0 || rot->dim > D) return DQ_ERR_SHAPE;
+    if (rot->rows <= 0) return DQ_ERR_INVALID_ARG;
+  }
+  if (q != nullptr) {
+    if (q_heads <= 0 || q_stride < q_heads * D || q_out_stride < q_heads * D ||
+        q_stride % unit || q_out_stride % 8)
+      return DQ_ERR_INVALID_ARG;
+    if (q_out == nullptr || !aligned(q, 16) || !aligned(q_out, 16)) return DQ_ERR_INVALID_ARG;
+    // in place only element by element
+    if (q_out == q && (dtype != DQ_BF16 || q_out_stride != q_stride)) return DQ_ERR_INVALID_ARG;
+  }
+  if (tokens == 0) return DQ_OK;
+  if (k == nullptr || v == nullptr || slots == nullptr || !aligned(k, 16) || !aligned(v, 16) ||
+      !aligned(slots, 8))
+    return DQ_ERR_INVALID_ARG;
+  if (rot != nullptr && (rot->cos == nullptr || rot->sin == nullptr || rot->positions == nullptr ||
+                         !aligned(rot->cos, 16) || !aligned(rot->sin, 16) ||
+                         !aligned(rot->positions, 4)))
+    return DQ_ERR_INVALID_ARG;
+  dq::AppendArgs A = {};
+  A.cache = *cache;
+  A.tokens = tokens;
+  A.k = k;
+  A.v = v;
+  A.q = q;
+  A.k_stride = k_stride;
+  A.v_stride = v_stride;
+  A.q_stride = q_stride;
+  A.q_out_stride = q_out_stride;
+  A.slots = slots;
+  if (rot != nullptr) A.rot = *rot;
+  A.q_heads = q != nullptr ? q_heads : 0;
+  A.q_out = q_out;
+  if (!dq::error_word(&A.err_word)) return DQ_ERR_CUDA;
+  return status_of(dq::launch_append(A, esize, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dq_paged_attention_workspace_bytes(const dq_kv_cache* cache, const dq_attention* args) {
+  dq::AttnArgs A = {};
+  if (check_attention(cache, args, &A.group) != DQ_OK) return 0;
+  A.cache = *cache;
+  A.a = *args;
+  return dq::attn_workspace_bytes(A);
+}
+
+dq_status dq_paged_attention(const dq_kv_cache* cache, const dq_attention* args, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  dq::AttnArgs A = {};
+  dq_status st = check_attention(cache, args, &A.group);
+  if (st != DQ_OK) return st;
+  if ((st = check_cache(cache, true)) != DQ_OK) return st;
+  const dq_attention& a = *args;
+  const int64_t width = (int64_t)a.heads * cache->head_dim;
+  if (a.q_stride < width || a.out_stride < width || a.q_stride % 8 || a.out_stride % 8 ||
+      !std::isfinite(a.scale))
+    return DQ_ERR_INVALID_ARG;
+  if (a.q_starts == nullptr && a.tokens != a.sequences) return DQ_ERR_INVALID_ARG;
+  if (a.tokens == 0 || a.sequences == 0 || a.max_q == 0) return DQ_OK;
+  if (a.table_stride < (a.max_len + cache->page_size - 1) / cache->page_size)
+    return DQ_ERR_INVALID_ARG;
+  if (a.q == nullptr || a.out == nullptr || a.lengths == nullptr ||
+      (a.page_table == nullptr && a.max_len > 0) || !aligned(a.q, 16) || !aligned(a.out, 16) ||
+      !aligned(a.q_starts, 4) || !aligned(a.lengths, 4) || !aligned(a.page_table, 4))
+    return DQ_ERR_INVALID_ARG;
+  A.cache = *cache;
+  A.a = a;
+  if (workspace == nullptr || workspace_bytes < dq::attn_workspace_bytes(A))
+    return DQ_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return DQ_ERR_INVALID_ARG;
+  if (!dq::error_word(&A.err_word)) return DQ_ERR_CUDA;
+  return status_of(dq::launch_attention(A, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -253,6 +253,149 @@ DQ_API dq_status dq_w4a4_linear(const void* X, int32_t dtype, int64_t T, int64_t
                                 dq_format fmt, float* y, int64_t ldy, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * 8-bit serving path: INT8 codes with one fp32 scale per row (token or output channel), the
+ * product of two such operands on the tensor cores, and the paged key/value cache with the
+ * attention that reads it. The rest of the inference path around the quantized linear layers
+ * (DualQuant appendix Table 11 lists attention, position rotation and the key/value cache
+ * beside the quantized products).
+ * fl32(..) is one IEEE binary32 operation, round to nearest even. */
+
+/* Row quantization to INT8: x~ = fl32(X * c) (c NULL: x~ = X); a = max |x~| of the row;
+ * d = max(fl32(a / 127), 2^-126), 0 for an all-zero row; q = RNE(fl32(x~ * fl32(1/d))), in
+ * -127..127 (0 for an all-zero row). Used on activations (rows are tokens, c the solver's
+ * column scales) and on weights (rows are output channels; pass the reciprocals of c).
+ *   X       device [rows, ldx] (dtype), 16-byte aligned, ldx*esize % 16 == 0, ldx >= n
+ *   c       device [n] fp32, 16-byte aligned, or NULL
+ *   codes   device out [rows, n] int8, 16-byte aligned
+ *   scales  device out [rows] fp32
+ * n must be a multiple of 16 (DQ_ERR_SHAPE). rows = 0 is allowed and does nothing. A row with a
+ * NaN or infinity gets codes 0 and the scale NaN and raises DQ_ERR_NONFINITE in the device
+ * error word. */
+DQ_API dq_status dq_row_quant(const void* X, int32_t dtype, int64_t rows, int64_t n, int64_t ldx,
+                              const float* c, int8_t* codes, float* scales, void* stream);
+
+/* Product of two INT8 operands with a scale per row:
+ *   y[t, i] = fl32(fl32(sum_j x[t, j] w[i, j]) * fl32(x_scales[t] * w_scales[i]))
+ * The integer sum is exact (int32), so the result does not depend on the order of summation.
+ *   x         device [T, K] int8, 16-byte aligned;  x_scales device [T] fp32
+ *   w         device [N, K] int8, 16-byte aligned;  w_scales device [N] fp32
+ *   y         device out [T, ldy], ldy >= N, of y_dtype (DQ_F32, or DQ_BF16: the fp32 value
+ *             rounded once more), aligned to its element
+ *   workspace device scratch of dq_w8a8_gemm_workspace_bytes(T, N, K) bytes, 16-byte aligned
+ * K must be a multiple of 16 and at most 131072 (so that no sum leaves int32): DQ_ERR_SHAPE.
+ * T = 0 is allowed and does nothing. */
+DQ_API size_t dq_w8a8_gemm_workspace_bytes(int64_t T, int64_t N, int64_t K);
+DQ_API dq_status dq_w8a8_gemm(const int8_t* x, const float* x_scales, int64_t T, const int8_t* w,
+                              const float* w_scales, int64_t N, int64_t K, void* y,
+                              int32_t y_dtype, int64_t ldy, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Linear layer on an 8-bit weight: dq_row_quant of X (rows are tokens, with c), then
+ * dq_w8a8_gemm with its codes; the result is bit-identical to those two calls. Arguments as
+ * theirs; the workspace (dq_w8a8_linear_workspace_bytes(T, N, K)) also holds the codes. */
+DQ_API size_t dq_w8a8_linear_workspace_bytes(int64_t T, int64_t N, int64_t K);
+DQ_API dq_status dq_w8a8_linear(const void* X, int32_t dtype, int64_t T, int64_t K, int64_t ldx,
+                                const float* c, const int8_t* w, const float* w_scales,
+                                int64_t N, void* y, int32_t y_dtype, int64_t ldy,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Element type of a paged cache: bf16, or INT8 codes with one fp32 scale per (token, head). */
+typedef enum { DQ_CACHE_BF16 = 0, DQ_CACHE_INT8 = 1 } dq_cache_kind;
+
+/* A paged key/value cache (device memory of the caller). Channel d of row r of head g in page p
+ * lies at element p*page_stride + g*head_stride + r*row_stride + d of k and of v, so pages can be
+ * kept head by head or token by token.
+ *   kind        dq_cache_kind
+ *   page_size   rows (tokens) of a page: 16, 32, 64, 128 or 256
+ *   head_dim    64 or 128
+ *   kv_heads, pages   >= 1
+ *   k, v        16-byte aligned; every stride a multiple of 16 bytes, row_stride >= head_dim
+ *   k_scales, v_scales   INT8: [pages, kv_heads, page_size] fp32, 16-byte aligned */
+typedef struct {
+  int32_t kind, page_size, head_dim, kv_heads;
+  int64_t pages;
+  void* k;
+  void* v;
+  int64_t page_stride, head_stride, row_stride;
+  float* k_scales;
+  float* v_scales;
+} dq_kv_cache;
+
+/* Position rotation: the first `dim` channels of a head in pairs (a, b) -> (fl32(fl32(a cos) -
+ * fl32(b sin)), fl32(fl32(b cos) + fl32(a sin))), pair i being channels i and i + dim/2, or, when
+ * `interleaved`, 2i and 2i + 1; the other channels are left as they are.
+ *   cos, sin   device [rows, dim/2] fp32, 16-byte aligned
+ *   positions  device [tokens] int32, each in [0, rows)
+ *   dim        a multiple of 8, at most head_dim */
+typedef struct {
+  const float* cos;
+  const float* sin;
+  const int32_t* positions;
+  int64_t rows;
+  int32_t dim, interleaved;
+} dq_rotary;
+
+/* Appends new tokens' keys and values to a paged cache, the keys rotated by their positions on
+ * the way; optionally rotates the tokens' queries in the same pass.
+ *   k, v    device, token t at t*k_stride (v_stride) elements: [kv_heads, head_dim] of dtype;
+ *           16-byte aligned, strides multiples of 16 bytes
+ *   slots   device [tokens] int64: token t goes to row slots[t] % page_size of page
+ *           slots[t] / page_size; a negative slot stores nothing (padding). Slots are distinct:
+ *           of two tokens with one slot, either may stay, or parts of both.
+ *   rot     NULL: no rotation
+ *   q       NULL, or like k with q_heads heads; q_out: device, token t at t*q_out_stride,
+ *           [q_heads, head_dim] bf16; may be q itself (bf16, same stride)
+ * bf16 cache: values are rounded to bf16. INT8 cache: each (token, head) row is quantized as by
+ * dq_row_quant over its head_dim channels, with its NaN and infinity rule. A slot or position out of
+ * range raises DQ_ERR_INVALID_ARG in the device error word and nothing of that token is
+ * written. The call leaves the cache's other rows as they are. */
+DQ_API dq_status dq_kv_append(const dq_kv_cache* cache, int64_t tokens, int32_t dtype,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              const int64_t* slots, const dq_rotary* rot, const void* q,
+                              int64_t q_stride, int32_t q_heads, void* q_out,
+                              int64_t q_out_stride, void* stream);
+
+/* Attention of new tokens over a paged cache that already holds their keys and values.
+ * Sequence b owns query tokens q_starts[b] .. q_starts[b+1]-1 (its last ones) and lengths[b]
+ * cache rows, row j in page page_table[b*table_stride + j / page_size]. For token i of n and
+ * head h: o = sum_j w_j v_j / sum_j w_j, w_j = exp(scale * q.k_j - max), over the rows
+ * j <= lengths[b] - n + i (causal), or j < lengths[b]; 0 where there is no such row. Query head h
+ * reads key head h / (heads / kv_heads).
+ *   q, out      device, token t at t*q_stride (out_stride) elements: [heads, head_dim] bf16,
+ *               16-byte aligned, strides multiples of 8
+ *   tokens      rows of q; tokens past q_starts[sequences] are neither read nor written
+ *   q_starts    device [sequences + 1] int32, or NULL (one token per sequence: tokens ==
+ *               sequences)
+ *   lengths     device [sequences] int32
+ *   page_table  device [sequences, table_stride] int32
+ *   max_q, max_len   host bounds of the new tokens and the rows of one sequence; what lies past
+ *               them is not computed, and raises DQ_ERR_INVALID_ARG in the device error word
+ * heads is a multiple of kv_heads, at most 128 times as many. Cache rows past a sequence's length may hold anything. A page
+ * number outside [0, pages) raises DQ_ERR_INVALID_ARG in the device error word (its rows count
+ * as zeros). Scores and softmax statistics are binary32; the weights of a tile are rounded to
+ * bf16 (bf16 cache) or fp16 (INT8 cache) for the product with v. */
+typedef struct {
+  const void* q;
+  void* out;
+  int64_t q_stride, out_stride;
+  int64_t tokens, sequences;
+  int32_t heads, causal;
+  const int32_t* q_starts;
+  const int32_t* lengths;
+  const int32_t* page_table;
+  int64_t table_stride;
+  int64_t max_q, max_len;
+  float scale;
+} dq_attention;
+
+/* Workspace (device bytes) of dq_paged_attention; depends on sizes only (the pointers in the
+ * arguments may be NULL). 0 for invalid arguments; at least 16 otherwise. */
+DQ_API size_t dq_paged_attention_workspace_bytes(const dq_kv_cache* cache,
+                                                 const dq_attention* args);
+DQ_API dq_status dq_paged_attention(const dq_kv_cache* cache, const dq_attention* args,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* Codecs used by the kernels, exposed for bit-exact tests (one code per output element). */
 typedef enum {
   DQ_CODEC_INT4 = 0,   /* RNE to -7..7, saturating; code = two's-complement nibble (uint8) */
