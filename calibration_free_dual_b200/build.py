@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdq.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["dq_api.cu", "dq_serve_api.cu", "dq_rows.cu", "dq_gemm8.cu", "dq_kv.cu",
-           "dq_attn.cu", "dq_solve.cu", "dq_solve_ext.cu", "dq_solve_int8.cu",
+           "dq_attn.cu", "dq_attn_tc.cu", "dq_solve.cu", "dq_solve_ext.cu", "dq_solve_int8.cu",
            "dq_solve_int8_ext.cu", "dq_act.cu", "dq_codec.cu", "dq_noalloc.cu", "dq_gemm.cu"]
 HEADERS = ["dq_device.cuh", "dq_internal.h", "dq_solve_kernel.cuh", "dq_gemm.h", "dq_tc.cuh",
            "dq_serve.h", "dq_attn.cuh"]

@@ -1,4 +1,5 @@
-// dq_attn.cu — attention of new tokens over a paged key/value cache: row tiles of 16.
+// dq_attn.cu — attention of new tokens over a paged key/value cache: the plan of a call, row tiles of
+// 16, and the join of split sequences.
 //
 // Rows are (token, query head) pairs that share a key head; a warp computes S = Q K^T for its 16 rows
 // and 16 cache rows at a time, keeps the running maximum and sum of each row (binary32, log2
@@ -478,24 +479,52 @@ attn_join_kernel(const AttnArgs A, const AttnPlan P) {
     *reinterpret_cast<uint32_t*>(dst + j) = pack2<false>(x[j] * inv, x[j + 1] * inv);
 }
 
+// Few (token, head) rows a key head: 16-row tiles, bound by the cache's bytes; more: 256-row tiles on
+// the tensor cores. Sequences are split where the row tiles do not fill the SMs.
 AttnPlan plan_attention(const AttnArgs& A, void* ws) {
   AttnPlan P = {};
   const dq_attention& a = A.a;
-  P.tile = 16;
-  P.row_tiles = (a.max_q * A.group + 15) / 16;
-  const int64_t base = P.row_tiles * A.cache.kv_heads * a.sequences;
-  // enough CTAs for every SM to hold two, none with less than 256 cache rows
-  const int64_t want = base > 0 ? (2 * SERVE_SMS + base - 1) / base : 1;
-  const int64_t most = std::max<int64_t>(1, a.max_len / 256);
-  P.splits = std::max<int64_t>(1, std::min(want, most));
-  P.chunk = std::max<int64_t>(64, ((a.max_len + P.splits - 1) / P.splits + 63) / 64 * 64);
+  const int64_t rows = a.max_q * A.group;
+  P.tile = rows <= 16 ? 16 : 256;
+  P.row_tiles = (rows + P.tile - 1) / P.tile;
+  const int64_t base = std::max<int64_t>(1, P.row_tiles * A.cache.kv_heads * a.sequences);
+  if (P.tile == 16) {
+    // enough CTAs for every SM to hold two, none with less than 256 cache rows
+    const int64_t want = (2 * SERVE_SMS + base - 1) / base;
+    const int64_t most = std::max<int64_t>(1, a.max_len / 256);
+    P.splits = std::max<int64_t>(1, std::min(want, most));
+    P.chunk = std::max<int64_t>(64, ((a.max_len + P.splits - 1) / P.splits + 63) / 64 * 64);
+  } else {
+    // one CTA per SM: the split with the least (waves) x (tiles of 128 cache rows + what a CTA spends
+    // besides, about 2 tiles' time, 4 when its result has to be joined)
+    const int64_t tiles = std::max<int64_t>(1, (a.max_len + 127) / 128);
+    int64_t best = 0, chunk = tiles;
+    for (int64_t s = 1; s <= std::min<int64_t>(tiles, 64); ++s) {
+      const int64_t per = (tiles + s - 1) / s;
+      const int64_t waves = (base * ((tiles + per - 1) / per) + SERVE_SMS - 1) / SERVE_SMS;
+      const int64_t cost = waves * (per + (s == 1 ? 2 : 4));
+      if (s == 1 || cost < best) {
+        best = cost;
+        chunk = per;
+      }
+    }
+    P.chunk = chunk * 128;
+  }
   P.splits = std::max<int64_t>(1, (a.max_len + P.chunk - 1) / P.chunk);
   if (P.splits > 1 && ws != nullptr) {
-    const int64_t rows = P.splits * a.tokens * a.heads;
+    const int64_t n = P.splits * a.tokens * a.heads;
     P.part_ml = static_cast<float2*>(ws);
-    P.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up((size_t)rows * 8, 256));
+    P.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up((size_t)n * 8, 256));
   }
   return P;
+}
+
+template <int D>
+cudaError_t launch_join(const AttnArgs& A, const AttnPlan& P, cudaStream_t s) {
+  const int64_t rows = A.a.max_q * A.a.heads;
+  attn_join_kernel<D><<<dim3((unsigned)((rows + 3) / 4), (unsigned)A.a.sequences), 128, 0, s>>>(A, P);
+  count_launches(1);
+  return cudaGetLastError();
 }
 
 template <int D, bool INT8>
@@ -508,11 +537,13 @@ cudaError_t launch_kind(const AttnArgs& A, const AttnPlan& P, cudaStream_t s) {
   if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
   K<<<dim3((unsigned)x, (unsigned)A.a.sequences), NT, R::SMEM, s>>>(A, P);
   count_launches(1);
-  if ((e = cudaGetLastError()) != cudaSuccess || P.splits == 1) return e;
-  const int64_t rows = A.a.max_q * A.a.heads;
-  attn_join_kernel<D><<<dim3((unsigned)((rows + 3) / 4), (unsigned)A.a.sequences), 128, 0, s>>>(A, P);
-  count_launches(1);
   return cudaGetLastError();
+}
+
+cudaError_t launch_rows(const AttnArgs& A, const AttnPlan& P, cudaStream_t s) {
+  const bool q8 = A.cache.kind == DQ_CACHE_INT8;
+  if (A.cache.head_dim == 64) return q8 ? launch_kind<64, true>(A, P, s) : launch_kind<64, false>(A, P, s);
+  return q8 ? launch_kind<128, true>(A, P, s) : launch_kind<128, false>(A, P, s);
 }
 
 }  // namespace
@@ -526,9 +557,9 @@ size_t attn_workspace_bytes(const AttnArgs& A) {
 
 cudaError_t launch_attention(const AttnArgs& A, void* workspace, cudaStream_t s) {
   const AttnPlan P = plan_attention(A, workspace);
-  const bool q8 = A.cache.kind == DQ_CACHE_INT8;
-  if (A.cache.head_dim == 64) return q8 ? launch_kind<64, true>(A, P, s) : launch_kind<64, false>(A, P, s);
-  return q8 ? launch_kind<128, true>(A, P, s) : launch_kind<128, false>(A, P, s);
+  const cudaError_t e = P.tile == 16 ? launch_rows(A, P, s) : launch_attention_tiles(A, P, s);
+  if (e != cudaSuccess || P.splits == 1) return e;
+  return A.cache.head_dim == 64 ? launch_join<64>(A, P, s) : launch_join<128>(A, P, s);
 }
 
 }  // namespace dq

@@ -16,8 +16,11 @@ struct AttnPlan {
   int tile;
   int64_t row_tiles, splits, chunk;
   float* part_o;          // splits > 1: [splits][tokens * heads][head_dim] fp32, unnormalised
-  float2* part_ml;        // [splits][tokens * heads] (maximum, log2 units; sum)
+  float2* part_ml;        // [splits][tokens * heads] (the exponent's reference, log2 units; sum)
 };
+
+// 256-row tiles on the tensor cores (dq_attn_tc.cu); partial results where P.splits > 1
+cudaError_t launch_attention_tiles(const AttnArgs& A, const AttnPlan& P, cudaStream_t s);
 
 namespace {
 

@@ -1,0 +1,635 @@
+// dq_attn_tc.cu — attention of new tokens over a paged key/value cache on the 5th-generation tensor
+// cores: row tiles of 256 (two of 128), 128 cache rows at a time.
+//
+// Rows are (token, query head) pairs that share a key head, so grouped heads fill a tile and read
+// each cache row once. Per CTA (one per SM), by warps:
+//   * 0-3 and 4-7, one per row tile, one thread per row: the tile's queries into shared memory; then
+//     for every 128 cache rows the scores S from tensor memory (TMEM), mask, running maximum, P = exp2(S - max)
+//     rounded and written back to TMEM over S. The output accumulates in TMEM; it is rescaled only
+//     when a row's maximum grows by more than 2^8 (the exponent's reference lags behind the
+//     maximum until then: weights stay below 2^8, sums and outputs are binary32);
+//   * 8: one lane issues the products (tcgen05.mma kind::f16): S_t = Q_t K^T from shared memory, then
+//     O_t += P_t V with P_t from TMEM. The two tiles alternate, so one's softmax runs under the
+//     other's products;
+//   * bf16 cache, 9: pages to shared memory by TMA (128-byte swizzle), K and V through a ring of four
+//     tiles;
+//   * INT8 cache, 12-15: codes to registers, exactly to fp16, to the same ring; per-row scales beside
+//     them. Keys' scales multiply the scores, values' scales the weights; the weights are kept
+//     relative to a running power of two above the values' scales (fp16's range).
+// Long sequences are split over CTAs when the row tiles do not fill the SMs (dq_attn.cu joins).
+// Every wait is bounded; on timeout the kernel raises the error word, frees its TMEM and returns.
+#include <algorithm>
+
+#include "dq_attn.cuh"
+#include "dq_internal.h"
+#include "dq_tc.cuh"
+
+namespace dq {
+namespace {
+
+constexpr unsigned FULL = 0xFFFFFFFFu;
+constexpr int KT = 128;                           // cache rows of a tile
+constexpr int SLOTS = 4;                          // K and V tiles in shared memory
+
+template <int D, bool INT8>
+struct Tc {
+  static constexpr int NT = INT8 ? 512 : 384;
+  // registers a thread, of the launch's (65536 / NT): softmax warps, products and TMA, conversion
+  static constexpr int R_SOFTMAX = INT8 ? 184 : 208, R_PRODUCT = INT8 ? 56 : 88, R_CONVERT = 88;
+  static constexpr int HALF = KT * 128;           // [128 rows][64 channels] of 2 bytes, swizzled
+  static constexpr int TILE = HALF * (D / 64);
+  static constexpr int Q_OFF = 0;                 // two row tiles
+  static constexpr int KV_OFF = 2 * TILE;
+  static constexpr int SC_OFF = KV_OFF + SLOTS * TILE;          // INT8: 4 x (k, v) scales
+  static constexpr int QF_OFF = SC_OFF + (INT8 ? 4 * 2 * KT * 4 + 4 * 16 : 0);   // query row factors
+  static constexpr int BAR_OFF = QF_OFF + (INT8 ? 2 * 128 * 4 : 0);
+  static constexpr int SMEM = BAR_OFF + 256 + 1024;
+  static constexpr uint32_t O_COL = 256;          // S_t at 128 t, O_t at 256 + D t
+};
+
+// A, B 16-bit (bf16 or fp16), D fp32; B K-major, or MN-major for V
+__host__ __device__ constexpr uint32_t idesc_f16(bool f16, int n, bool b_mn) {
+  return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+// 32 columns without a wait
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+         "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+         "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+         "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+         "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
+  // MN-major, 128-byte swizzle: 64-channel blocks a half tile apart, 8-row groups 1024 bytes
+  return smem_desc(addr, KT * 128, 1024, 2);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+__device__ __forceinline__ float f_of(uint32_t u) { return __uint_as_float(u); }
+
+template <int N> __device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
+}
+
+constexpr float GROW = 8.0f;                      // log2 of the largest weight before a rescale
+// values' scales are followed from 2^-80 (the sums of weights up to 2^95 stay in binary32) to 2^90 (weights
+// down to 2^-39 of the largest stay normal)
+constexpr float V_LOW = -80.0f, V_HIGH = 90.0f;
+constexpr float V_HEAD = 7.0f;                    // INT8: weights * values' scales stay below 2^(GROW + V_HEAD)
+
+template <int D, bool INT8>
+__global__ void __launch_bounds__(Tc<D, INT8>::NT, 1)
+attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const AttnArgs A, const AttnPlan P) {
+  using T = Tc<D, INT8>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const dq_attention& a = A.a;
+  const dq_kv_cache& C = A.cache;
+  const int G = C.kv_heads, group = A.group;
+  // the last row tiles (which see the most cache rows) go first
+  const int64_t idx = blockIdx.x;
+  const int split = (int)(idx % P.splits);
+  const int g = (int)(idx / P.splits % G);
+  const int64_t rt = P.row_tiles - 1 - idx / P.splits / G;
+  const int b = blockIdx.y;
+  const SeqBounds sq = seq_bounds(a, b);
+  if (sq.bad && idx == 0 && tid == 0) atomicOr(A.err_word, ERRBIT_BADARG);
+  const int64_t rows = (int64_t)sq.n * group, row0 = rt * 256;
+  if (row0 >= rows) return;
+  const int64_t kb = split * P.chunk;
+  if (split > 0 && kb >= sq.len) return;
+  // tiles of cache rows that the two row tiles see
+  int nt[2];
+  const int64_t chunk_end = min64(sq.len, kb + P.chunk);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int64_t first = row0 + 128 * t, last = min64(first + 127, rows - 1);
+    const int64_t ke = first < rows ? min64(chunk_end, visible(a, sq, (int)(last / group))) : 0;
+    nt[t] = ke > kb ? (int)((ke - kb + KT - 1) / KT) : 0;
+  }
+  const int n = max(nt[0], nt[1]);
+
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  unsigned char* base = smem_raw + (sbase - raw);
+  const uint32_t full0 = sbase + T::BAR_OFF, empty0 = full0 + 8 * SLOTS;
+  const uint32_t sfull0 = empty0 + 8 * SLOTS, pready0 = sfull0 + 16, ofull0 = pready0 + 16;
+  const uint32_t qready = ofull0 + 16, vtail = qready + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + T::BAR_OFF + 8 * (2 * SLOTS + 8));
+  volatile int* fail = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  if (warp == 8) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (tid == 0) {
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(full0 + 8 * s, INT8 ? 4 : 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(sfull0 + 8 * t, 1);
+      mbar_init(pready0 + 8 * t, 4);
+      mbar_init(ofull0 + 8 * t, 1);
+    }
+    mbar_init(qready, 8);
+    mbar_init(vtail, 1);
+    *fail = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const bool tail = kb + (int64_t)n * KT > sq.len;     // the last tile reaches past the sequence
+
+  if (warp < 8) {
+    more_registers<T::R_SOFTMAX>();
+    // ================================================================= softmax, one thread a row
+    const int t = warp >> 2, sp = warp & 3;
+    const int r = sp * 32 + lane;
+    const int64_t row = row0 + 128 * t + r;
+    const bool there = row < rows;
+    // ---- queries of the row tile: 16-byte chunks, a row by D/8 threads
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // (the exponent's factor is positive)
+    float* qfac = reinterpret_cast<float*>(base + T::QF_OFF);
+    {
+      constexpr int CPR = D / 8;
+      const int ch = lane % CPR;
+#pragma unroll 4
+      for (int i = 0; i < 32 / (32 / CPR); ++i) {
+        const int qr = sp * 32 + i * (32 / CPR) + lane / CPR;
+        const int64_t qrow = row0 + 128 * t + qr;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (qrow < rows) {
+          const int64_t tok = sq.start + qrow / group;
+          const int h = g * group + (int)(qrow % group);
+          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_stride + (int64_t)h * D) + ch);
+        }
+        uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
+        if constexpr (INT8) {
+          float mx = 0.0f;
+          float2 f[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[j] = bf16x2_to_f2(w[j]);
+            mx = fmaxf(mx, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
+          }
+#pragma unroll
+          for (int off = 1; off < CPR; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
+          const float fac = f16_row_factor(mx);
+          if (ch == 0) qfac[128 * t + qr] = fac;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = pack16<true>(f[j].x * fac, f[j].y * fac);
+        }
+        *reinterpret_cast<uint4*>(base + T::Q_OFF + t * T::TILE + (ch >> 3) * T::HALF + qr * 128 +
+                                  (((ch & 7) ^ (qr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qready);
+    }
+    // cache rows this row sees, from the CTA's first on
+    const int lim = there ? (int)(min64(chunk_end, visible(a, sq, (int)(row / group))) - kb) : 0;
+    const bool warp_there = row0 + 128 * t + sp * 32 < rows;
+    float c = fabsf(a.scale) * 1.4426950408889634f;
+    if (INT8) c /= qfac[128 * t + r];
+    c = fmaxf(c, 1e-37f);                          // (a masked score stays -inf)
+    const uint32_t s_addr = tmem + ((uint32_t)(sp * 32) << 16) + 128 * t;
+    const uint32_t o_addr = tmem + ((uint32_t)(sp * 32) << 16) + T::O_COL + D * t;
+    float ref = -INFINITY;                          // exponent's reference: weights are exp2(c s - ref)
+    float l = 0.0f, vlog = V_LOW;                   // INT8: log2 of the values' unit
+    bool ok = true;
+    for (int j = 0; j < nt[t]; ++j) {
+      if (!mbar_wait(sfull0 + 8 * t, (uint32_t)j & 1u) || *fail) { ok = false; break; }
+      tc_fence_after();
+      if (warp_there) {
+        const int left = lim - j * KT;               // columns from here on are masked
+        const bool masked = __any_sync(FULL, left < KT);
+        const float* ks = reinterpret_cast<const float*>(base + T::SC_OFF) + (j & 3) * 2 * KT;
+        const float* vs = ks + KT;
+        // ---- the row's scores, mask, maximum
+        uint32_t s[KT];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32_async(s_addr + 32 * q, s + 32 * q);
+        tmem_wait_ld();
+        if constexpr (INT8) {
+#pragma unroll
+          for (int i = 0; i < KT; i += 4) {
+            const float4 k4 = *reinterpret_cast<const float4*>(ks + i);
+            const float2 x0 = mul2(make_float2(f_of(s[i]), f_of(s[i + 1])), make_float2(k4.x, k4.y));
+            const float2 x1 = mul2(make_float2(f_of(s[i + 2]), f_of(s[i + 3])), make_float2(k4.z, k4.w));
+            s[i] = __float_as_uint(x0.x); s[i + 1] = __float_as_uint(x0.y);
+            s[i + 2] = __float_as_uint(x1.x); s[i + 3] = __float_as_uint(x1.y);
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < KT; ++i)
+            if (i >= left) s[i] = 0xFF800000u;
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < KT; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            m4[e] = fmaxf(m4[e], fmaxf(f_of(s[i + 2 * e]), f_of(s[i + 2 * e + 1])));
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        mx *= c;
+        float vl = vlog;
+        if constexpr (INT8) {
+          const float4 vm = *reinterpret_cast<const float4*>(base + T::SC_OFF + 4 * 2 * KT * 4 + (j & 3) * 16);
+          const float top = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
+          vl = fmaxf(vl, fminf((float)((int)(__float_as_uint(top) >> 23) - 126), V_HIGH));
+          if (!(top > 0.0f)) vl = vlog;
+        }
+        // ---- move the reference when the weights could outgrow it
+        const float want = INT8 ? mx + vl - V_HEAD : mx;
+        if (j == 0) {
+          ref = mx == -INFINITY ? 0.0f : want;
+        } else if (__any_sync(FULL, want > ref + GROW)) {
+          float al = 1.0f;
+          if (want > ref) {
+            al = exp2_fast(ref - want);
+            ref = want;
+          }
+          l *= al;
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32_async(o_addr + 32 * q, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(f_of(o[i]) * al);
+            tmem_st32_async(o_addr + 32 * q, o);
+          }
+          tmem_wait_st();
+        }
+        vlog = vl;
+        // ---- weights, over the scores' columns (all of which have been read)
+        float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
+        const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const uint32_t* x = s + 64 * q + i;
+            float2 y0 = fma2(make_float2(f_of(x[0]), f_of(x[1])), c2, r2);
+            float2 y1 = fma2(make_float2(f_of(x[2]), f_of(x[3])), c2, r2);
+            y0.x = exp2_fast(y0.x); y0.y = exp2_fast(y0.y);
+            y1.x = exp2_fast(y1.x); y1.y = exp2_fast(y1.y);
+            l0 = __fadd2_rn(l0, y0);
+            l1 = __fadd2_rn(l1, y1);
+            if constexpr (INT8) {
+              const float4 v4 = *reinterpret_cast<const float4*>(vs + 64 * q + i);
+              y0 = mul2(y0, make_float2(v4.x, v4.y));
+              y1 = mul2(y1, make_float2(v4.z, v4.w));
+            }
+            p[i / 2] = pack16<INT8>(y0.x, y0.y);
+            p[i / 2 + 1] = pack16<INT8>(y1.x, y1.y);
+          }
+          tmem_st32_async(s_addr + 32 * q, p);
+        }
+        l += (l0.x + l0.y) + (l1.x + l1.y);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pready0 + 8 * t);
+    }
+    // ---- the output
+    if (ok && nt[t] > 0) ok = mbar_wait(ofull0 + 8 * t, 0) && !*fail;
+    if (ok && warp_there) {
+      tc_fence_after();
+      const int64_t tok = sq.start + (there ? row / group : 0);
+      const int h = g * group + (int)(there ? row % group : 0);
+      const bool none = nt[t] == 0;
+      const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+      const int64_t at = ((int64_t)split * a.tokens + tok) * a.heads + h;
+      if (P.splits > 1 && there) P.part_ml[at] = make_float2(none || l == 0.0f ? -INFINITY : ref, l);
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        if (none) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        } else {
+          tmem_ld32_async(o_addr + 32 * q, o);
+          tmem_wait_ld();
+        }
+        if (!there) continue;
+        if (P.splits == 1) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + (int64_t)h * D + 32 * q);
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)       // (a row that sees nothing has no sum: its output is 0)
+            w[i] = l == 0.0f ? 0u : pack16<false>(f_of(o[2 * i]) * inv, f_of(o[2 * i + 1]) * inv);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(P.part_o + at * D + 32 * q);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      tc_fence_before();
+    }
+    if (!ok) *fail = 1;
+  } else if (warp < 12) {
+    fewer_registers<T::R_PRODUCT>();
+    if (warp == 8) {
+    // ================================================================= products
+    if (lane == 0 && n > 0) {
+      const uint32_t ID_S = idesc_f16(INT8, KT, false), ID_O = idesc_f16(INT8, D, true);
+      auto scores = [&](int t, int slot) {
+        const uint32_t q = sbase + T::Q_OFF + t * T::TILE, k = sbase + T::KV_OFF + slot * T::TILE;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          mma_ss(tmem + 128 * t, operand_desc(q + (s >> 2) * T::HALF + 32 * (s & 3)),
+                 operand_desc(k + (s >> 2) * T::HALF + 32 * (s & 3)), ID_S, s > 0);
+        mma_commit(sfull0 + 8 * t);
+      };
+      auto outputs = [&](int t, int slot, bool first) {
+        const uint32_t v = sbase + T::KV_OFF + slot * T::TILE;
+#pragma unroll
+        for (int s = 0; s < KT / 16; ++s)
+          mma_ts(tmem + T::O_COL + D * t, tmem + 128 * t + 8 * s, v_desc(v + 2048 * s), ID_O, !first || s > 0);
+      };
+      bool ok = mbar_wait(qready, 0) && mbar_wait(full0, 0) && !*fail;
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < 2; ++t)
+          if (nt[t] > 0) scores(t, 0);
+        mma_commit(empty0);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int vi = 2 * j + 1, ki = 2 * j + 2;
+        const int vslot = vi % SLOTS, kslot = ki % SLOTS;
+        bool v_here = false, k_here = false;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (j < nt[t]) {
+            ok = mbar_wait(pready0 + 8 * t, (uint32_t)j & 1u) && !*fail;
+            if (ok && !v_here) {
+              ok = mbar_wait(full0 + 8 * vslot, (uint32_t)(vi / SLOTS) & 1u) && !*fail;
+              if (ok && !INT8 && tail && j == n - 1) ok = mbar_wait(vtail, 0) && !*fail;
+              v_here = true;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            outputs(t, vslot, j == 0);
+            if (j == nt[t] - 1) mma_commit(ofull0 + 8 * t);
+          }
+          if (j + 1 < nt[t]) {
+            if (!k_here) ok = mbar_wait(full0 + 8 * kslot, (uint32_t)(ki / SLOTS) & 1u) && !*fail;
+            k_here = true;
+            if (!ok) break;
+            tc_fence_after();
+            scores(t, kslot);
+          }
+        }
+        if (!ok) break;
+        mma_commit(empty0 + 8 * vslot);
+        if (j + 1 < n) mma_commit(empty0 + 8 * kslot);
+      }
+      if (!ok) *fail = 1;
+    }
+    } else if (!INT8 && warp == 9) {
+    // ================================================================= pages by TMA
+    const int box = C.page_size < KT ? C.page_size : KT;
+    const int boxes = KT / box;
+    const int* table = a.page_table + b * a.table_stride;
+    bool ok = true;
+    int i = 0;
+    for (; i < 2 * n && ok; ++i) {
+      const int slot = i % SLOTS;
+      const int64_t key0 = kb + (int64_t)(i >> 1) * KT;
+      const uint32_t bar = full0 + 8 * slot;
+      // pages with a row of the sequence (rows past them keep what was there)
+      const int live = min(boxes, (int)((sq.len - key0 + box - 1) / box));
+      int page = 0;
+      if (lane < live) {
+        page = __ldg(table + (key0 + lane * box) / C.page_size);
+        if (page < 0 || page >= C.pages) {
+          atomicOr(A.err_word, ERRBIT_BADARG);
+          page = (int)C.pages;                      // outside the map: zeros
+        }
+      }
+      int got = 1;
+      if (lane == 0) {
+        got = mbar_wait(empty0 + 8 * slot, ((uint32_t)(i / SLOTS) & 1u) ^ 1u) && !*fail;
+        if (got) mbar_expect_tx(bar, (uint32_t)live * box * D * 2);
+      }
+      ok = __shfl_sync(FULL, got, 0) != 0;
+      if (ok && lane < live) {
+        const uint32_t dst = sbase + T::KV_OFF + slot * T::TILE + lane * box * 128;
+        const int prow = (int)((key0 + lane * box) % C.page_size);
+        for (int h = 0; h < D / 64; ++h)
+          tma_load_4d(dst + h * T::HALF, (i & 1) ? &tmV : &tmK, 64 * h, prow, g, page, bar);
+      }
+    }
+    if (!ok) {
+      *fail = 1;
+      --i;                                           // this tile's copies were not issued
+    }
+    // zeros for the values past the sequence, which may be anything (0 * NaN)
+    if (ok && tail && n > 0) {
+      const int li = 2 * n - 1, slot = li % SLOTS;
+      int got = 1;
+      if (lane == 0) got = mbar_wait(full0 + 8 * slot, (uint32_t)(li / SLOTS) & 1u) && !*fail;
+      if (__shfl_sync(FULL, got, 0)) {
+        const int valid = (int)(sq.len - (kb + (int64_t)(n - 1) * KT));
+        for (int e = valid * 8 + lane; e < KT * 8; e += 32)
+          for (int h = 0; h < D / 64; ++h)
+            *reinterpret_cast<uint4*>(base + T::KV_OFF + slot * T::TILE + h * T::HALF + e * 16) = make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vtail);
+      } else {
+        *fail = 1;
+      }
+    }
+    // on failure, copies in flight land before the CTA ends
+    if (*fail && lane == 0)
+      for (int k = i > SLOTS ? i - SLOTS : 0; k < i; ++k)
+        mbar_wait(full0 + 8 * (k % SLOTS), (uint32_t)(k / SLOTS) & 1u);
+    }
+  } else if constexpr (INT8) {
+    fewer_registers<T::R_CONVERT>();
+    // ================================================================= codes to fp16
+    constexpr int CPR = D / 16, RPP = 128 / CPR, ROUNDS = KT / RPP;   // 16 codes per thread and round
+    const int w = tid - 12 * 32, ch = w % CPR, r0 = w / CPR;
+    const int* table = a.page_table + b * a.table_stride;
+    uint4 next[ROUNDS];
+    float nks = 0.0f, nvs = 0.0f;
+    auto page_at = [&](int64_t key) -> int64_t {      // -1: no such row
+      if (key >= sq.len) return -1;
+      const int page = __ldg(table + key / C.page_size);
+      if (page < 0 || page >= C.pages) {
+        atomicOr(A.err_word, ERRBIT_BADARG);
+        return -1;
+      }
+      return page;
+    };
+    auto fetch = [&](int i) {
+      const int64_t key0 = kb + (int64_t)(i >> 1) * KT;
+      const int8_t* src = static_cast<const int8_t*>((i & 1) ? C.v : C.k);
+#pragma unroll
+      for (int x = 0; x < ROUNDS; ++x) {
+        const int64_t key = key0 + r0 + x * RPP;
+        const int64_t page = page_at(key);
+        next[x] = make_uint4(0, 0, 0, 0);
+        if (page >= 0)
+          next[x] = __ldg(reinterpret_cast<const uint4*>(src + page * C.page_stride + (int64_t)g * C.head_stride +
+                                                         (key % C.page_size) * C.row_stride) + ch);
+      }
+      if (!(i & 1)) {
+        const int64_t key = key0 + w, page = page_at(key);
+        nks = nvs = 0.0f;
+        if (page >= 0) {
+          const int64_t at = (page * G + g) * C.page_size + key % C.page_size;
+          nks = __ldg(C.k_scales + at);
+          nvs = __ldg(C.v_scales + at);
+        }
+      }
+    };
+    bool ok = true;
+    if (n > 0) fetch(0);
+    for (int i = 0; i < 2 * n && ok; ++i) {
+      const int slot = i % SLOTS;
+      uint4 cur[ROUNDS];
+#pragma unroll
+      for (int x = 0; x < ROUNDS; ++x) cur[x] = next[x];
+      const float cks = nks, cvs = nvs;
+      if (i + 1 < 2 * n) fetch(i + 1);
+      ok = mbar_wait(empty0 + 8 * slot, ((uint32_t)(i / SLOTS) & 1u) ^ 1u) && !*fail;
+      if (!ok) break;
+      unsigned char* tile = base + T::KV_OFF + slot * T::TILE + (ch >> 2) * T::HALF;
+#pragma unroll
+      for (int x = 0; x < ROUNDS; ++x) {
+        const int r = r0 + x * RPP;
+        const uint32_t u[4] = {cur[x].x ^ 0x80808080u, cur[x].y ^ 0x80808080u, cur[x].z ^ 0x80808080u, cur[x].w ^ 0x80808080u};
+        uint4* row = reinterpret_cast<uint4*>(tile + r * 128);
+        row[(2 * (ch & 3)) ^ (r & 7)] = make_uint4(codes_lo_f16(u[0]), codes_hi_f16(u[0]), codes_lo_f16(u[1]), codes_hi_f16(u[1]));
+        row[(2 * (ch & 3) + 1) ^ (r & 7)] = make_uint4(codes_lo_f16(u[2]), codes_hi_f16(u[2]), codes_lo_f16(u[3]), codes_hi_f16(u[3]));
+      }
+      if (!(i & 1)) {
+        // the scales of tile j outlive its K slot: four sets, the fourth next one is written only
+        // after both softmaxes have passed this one
+        const int j = i >> 1;
+        float* sc = reinterpret_cast<float*>(base + T::SC_OFF) + (j & 3) * 2 * KT;
+        sc[w] = cks;
+        sc[KT + w] = cvs;
+        float mx = cvs;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
+        if (lane == 0) reinterpret_cast<float*>(base + T::SC_OFF + 4 * 2 * KT * 4)[(j & 3) * 4 + w / 32] = mx;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full0 + 8 * slot);
+    }
+    if (!ok) *fail = 1;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *fail) atomicOr(A.err_word, ERRBIT_TIMEOUT);
+  if (warp == 8) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// [pages][kv_heads][page_size][head_dim] bf16 with the cache's strides, box of 64 channels x (at
+// most 128) rows, 128-byte swizzle, zeros outside
+bool cache_map(CUtensorMap* map, const dq_kv_cache& C, const void* p) {
+  EncodeTiledFn fn = encoder();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)C.head_dim, (cuuint64_t)C.page_size, (cuuint64_t)C.kv_heads, (cuuint64_t)C.pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)C.row_stride * 2, (cuuint64_t)C.head_stride * 2, (cuuint64_t)C.page_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)std::min(C.page_size, KT), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool INT8>
+cudaError_t launch_kind(const AttnArgs& A, const AttnPlan& P, cudaStream_t s) {
+  using T = Tc<D, INT8>;
+  constexpr auto K = attn_tiles_kernel<D, INT8>;
+  cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+  if (e != cudaSuccess) return e;
+  alignas(64) CUtensorMap tk = {}, tv = {};
+  if (!INT8 && (!cache_map(&tk, A.cache, A.cache.k) || !cache_map(&tv, A.cache, A.cache.v)))
+    return cudaErrorInvalidValue;
+  const int64_t x = P.splits * A.cache.kv_heads * P.row_tiles;
+  if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
+  K<<<dim3((unsigned)x, (unsigned)A.a.sequences), T::NT, T::SMEM, s>>>(tk, tv, A, P);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tiles(const AttnArgs& A, const AttnPlan& P, cudaStream_t s) {
+  const bool q8 = A.cache.kind == DQ_CACHE_INT8;
+  if (A.cache.head_dim == 64) return q8 ? launch_kind<64, true>(A, P, s) : launch_kind<64, false>(A, P, s);
+  return q8 ? launch_kind<128, true>(A, P, s) : launch_kind<128, false>(A, P, s);
+}
+
+}  // namespace dq

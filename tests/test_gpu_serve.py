@@ -5,12 +5,14 @@ binary32 operations, so they agree bit for bit (bf16 results after one more roun
 
 Attention, per output: the result is rounded to bf16 (half a step: 2^-8 of its value), each
 weight before the product with v to bf16 or, for the INT8 cache, fp16 (2^-8 or 2^-11 of itself, so of
-mag = sum w|v| / sum w in all; fp16 weights below 2^-39 of the largest round to a multiple of
-that), and a score is off by e = (D + 8) 2^-23 max_j scale sum_d |q k| (binary32 sums and
-products), which changes a weight by a factor within 1 +- 2e (numerator and denominator). The
-exponential (2^-22), the sums and the joins of up to a few hundred parts stay within
-2^-15 of mag. Bound: 2^-8 |o| + mag (w + 4 e + 2^-15), the cross term of the first two included
-by 1.02.
+mag = sum w|v| / sum w in all), and a score is off by e = (D + 8) 2^-23 max_j scale sum_d |q k|
+(binary32 sums and products), which changes a weight by a factor within 1 +- 2e (numerator and
+denominator). The exponential (2^-22), the sums and the joins of up to a few hundred parts stay
+within 2^-15 of mag. fp16 weights are weight * value scale * 2^7 / M at the least, M a power of two
+at most twice the largest value scale: below fp16's normal range they round to multiples of 2^-24, an
+error of up to 2^-25 2^-7 M 127 <= 2^-31 max|v| per cache row beside the largest weight 1, which the
+sum of the weights is at least. Bound: 1.02 (2^-8 |o| + mag (w + 4 e + 2^-15)) +
+m 2^-31 max|v|, the factor for the cross term of the first two.
 """
 import numpy as np
 import pytest
@@ -359,7 +361,7 @@ def _check_attention(o, q, cache, table, lens, news, causal, scale=None):
         # every weight over their sum moves by a factor within exp(+-2e), and exp(2e) - 1 <= 4e up to
         # e = 0.6 (exp(1.2) - 1 = 2.32 < 2.4; convex, equal at 0)
         assert e.max(initial=0.0) < 0.6
-        bound = 1.02 * (2.0 ** -8 * np.abs(ref) + mag * (w + 4 * e + 2.0 ** -15)) + m * 2.0 ** -39 * np.abs(v).max(initial=0.0)
+        bound = 1.02 * (2.0 ** -8 * np.abs(ref) + mag * (w + 4 * e + 2.0 ** -15)) + m * 2.0 ** -31 * np.abs(v).max(initial=0.0)
         err = np.abs(got[at:at + n] - ref)
         assert np.all(err <= bound), (b, n, m, float(np.nanmax(err / np.maximum(bound, 1e-30))))
         at += n
