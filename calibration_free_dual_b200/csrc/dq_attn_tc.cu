@@ -8,13 +8,12 @@
 //     rounded and written back to TMEM over S. The output accumulates in TMEM; it is rescaled only
 //     when a row's maximum grows by more than 2^8 (the exponent's reference lags behind the
 //     maximum until then: weights stay below 2^8, sums and outputs are binary32);
-//   * 8: one lane issues the products (tcgen05.mma kind::f16): S_t = Q_t K^T from shared memory, then
+//   * 8: issues the products (tcgen05.mma kind::f16): S_t = Q_t K^T from shared memory, then
 //     O_t += P_t V with P_t from TMEM. The two tiles alternate, so one's softmax runs under the
 //     other's products;
-//   * bf16 cache, 9: pages to shared memory by TMA (128-byte swizzle), K and V through a ring of four
-//     tiles;
-//   * INT8 cache, 12-15: codes to registers, exactly to fp16, to the same ring; per-row scales beside
-//     them. Keys' scales multiply the scores, values' scales the weights; the weights are kept
+//   * 9: pages by TMA, K and V in turn: bf16 with the 128-byte swizzle straight to a ring of four tiles;
+//   * INT8 cache, 12-15: codes from a ring of their own, exactly to fp16, to the ring of tiles; per-row
+//     scales beside them. Keys' scales multiply the scores, values' scales the weights; the weights are kept
 //     relative to a running power of two above the values' scales (fp16's range).
 // Long sequences are split over CTAs when the row tiles do not fill the SMs (dq_attn.cu joins).
 // Every wait is bounded; on timeout the kernel raises the error word, frees its TMEM and returns.
@@ -29,40 +28,45 @@ namespace {
 
 constexpr unsigned FULL = 0xFFFFFFFFu;
 constexpr int KT = 128;                           // cache rows of a tile
-constexpr int SLOTS = 4;                          // K and V tiles in shared memory
 
 template <int D, bool INT8>
 struct Tc {
   static constexpr int NT = INT8 ? 512 : 384;
   // registers a thread, of the launch's (65536 / NT): softmax warps, products and TMA, conversion
-  static constexpr int R_SOFTMAX = INT8 ? 184 : 208, R_PRODUCT = INT8 ? 56 : 88, R_CONVERT = 88;
+  static constexpr int R_SOFTMAX = INT8 ? 184 : 208, R_PRODUCT = INT8 ? 56 : 88;
+  static constexpr int R_CONVERT = 88;
+  static constexpr int SLOTS = INT8 ? 3 : 4;      // K and V tiles in shared memory
+  static constexpr int RAW_SLOTS = INT8 ? 3 : 0;  // tiles of codes on their way to them
   static constexpr int HALF = KT * 128;           // [128 rows][64 channels] of 2 bytes, swizzled
   static constexpr int TILE = HALF * (D / 64);
+  static constexpr int RAW = KT * D;
   static constexpr int Q_OFF = 0;                 // two row tiles
   static constexpr int KV_OFF = 2 * TILE;
-  static constexpr int SC_OFF = KV_OFF + SLOTS * TILE;          // INT8: 4 x (k, v) scales
+  static constexpr int RAW_OFF = KV_OFF + SLOTS * TILE;
+  static constexpr int SC_OFF = RAW_OFF + RAW_SLOTS * RAW;      // INT8: 4 x (k, v) scales, maxima
   static constexpr int QF_OFF = SC_OFF + (INT8 ? 4 * 2 * KT * 4 + 4 * 16 : 0);   // query row factors
   static constexpr int BAR_OFF = QF_OFF + (INT8 ? 2 * 128 * 4 : 0);
   static constexpr int SMEM = BAR_OFF + 256 + 1024;
   static constexpr uint32_t O_COL = 256;          // S_t at 128 t, O_t at 256 + D t
 };
+static_assert(Tc<128, true>::SMEM <= 227 * 1024 && Tc<128, false>::SMEM <= 227 * 1024, "shared memory");
 
 // A, B 16-bit (bf16 or fp16), D fp32; B K-major, or MN-major for V
 __host__ __device__ constexpr uint32_t idesc_f16(bool f16, int n, bool b_mn) {
   return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t elected) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(elected) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t elected) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(elected) : "memory");
 }
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             int z, int w, uint32_t bar) {
@@ -118,6 +122,28 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 __device__ __forceinline__ float f_of(uint32_t u) { return __uint_as_float(u); }
 
+constexpr int POLY = 2;                           // of 8 groups of four weights, those with a pair by polynomial
+constexpr float C0 = 0.9999992847442627f, C1 = 0.6931217908859253f, C2 = 0.240247443318367f,
+                C3 = 0.05591785907745361f, C4 = 0.009570102207362652f;
+// 2^y of a pair by the FMA pipe: y = n + f with n the nearest integer (added and removed 1.5 2^23), 2^f on
+// [-1/2, 1/2] by a polynomial of degree 4 (fitted to the least relative error, 2.7e-6 in binary32), n added to
+// the exponent. y below -125 counts as -125 (2^-125: nothing beside a weight).
+__device__ __forceinline__ float2 exp2_poly(float2 y) {
+  y.x = fmaxf(y.x, -125.0f);
+  y.y = fmaxf(y.y, -125.0f);
+  const float2 magic = make_float2(12582912.0f, 12582912.0f), back = make_float2(-12582912.0f, -12582912.0f);
+  const float2 t = __fadd2_rn(y, magic);
+  const float2 n = __fadd2_rn(t, back);
+  const float2 f = fma2(n, make_float2(-1.0f, -1.0f), y);
+  float2 p = make_float2(C4, C4);
+  p = fma2(p, f, make_float2(C3, C3));
+  p = fma2(p, f, make_float2(C2, C2));
+  p = fma2(p, f, make_float2(C1, C1));
+  p = fma2(p, f, make_float2(C0, C0));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
 template <int N> __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
 }
@@ -136,6 +162,7 @@ __global__ void __launch_bounds__(Tc<D, INT8>::NT, 1)
 attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const AttnArgs A, const AttnPlan P) {
   using T = Tc<D, INT8>;
+  constexpr int SLOTS = T::SLOTS;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const dq_attention& a = A.a;
@@ -169,8 +196,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   unsigned char* base = smem_raw + (sbase - raw);
   const uint32_t full0 = sbase + T::BAR_OFF, empty0 = full0 + 8 * SLOTS;
   const uint32_t sfull0 = empty0 + 8 * SLOTS, pready0 = sfull0 + 16, ofull0 = pready0 + 16;
-  const uint32_t qready = ofull0 + 16, vtail = qready + 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + T::BAR_OFF + 8 * (2 * SLOTS + 8));
+  const uint32_t phalf0 = ofull0 + 16, qready = phalf0 + 16, vtail = qready + 8;
+  const uint32_t rawfull0 = vtail + 8, rawempty0 = rawfull0 + 8 * T::RAW_SLOTS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + T::BAR_OFF + 8 * (2 * SLOTS + 10 + 2 * T::RAW_SLOTS));
   volatile int* fail = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   if (warp == 8) tmem_alloc(smem_u32(tmem_slot), 512);
@@ -182,7 +210,12 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     for (int t = 0; t < 2; ++t) {
       mbar_init(sfull0 + 8 * t, 1);
       mbar_init(pready0 + 8 * t, 4);
+      mbar_init(phalf0 + 8 * t, 4);
       mbar_init(ofull0 + 8 * t, 1);
+    }
+    for (int s = 0; s < T::RAW_SLOTS; ++s) {
+      mbar_init(rawfull0 + 8 * s, 1);
+      mbar_init(rawempty0 + 8 * s, 4);
     }
     mbar_init(qready, 8);
     mbar_init(vtail, 1);
@@ -329,7 +362,13 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             const uint32_t* x = s + 64 * q + i;
             float2 y0 = fma2(make_float2(f_of(x[0]), f_of(x[1])), c2, r2);
             float2 y1 = fma2(make_float2(f_of(x[2]), f_of(x[3])), c2, r2);
-            y0.x = exp2_fast(y0.x); y0.y = exp2_fast(y0.y);
+            // the exponential unit gives 16 results a clock to the SM, as long for a tile as its
+            // products take: part of the pairs goes to the FMA pipe
+            if ((i / 2) % 16 < 2 * POLY) {
+              y0 = exp2_poly(y0);
+            } else {
+              y0.x = exp2_fast(y0.x); y0.y = exp2_fast(y0.y);
+            }
             y1.x = exp2_fast(y1.x); y1.y = exp2_fast(y1.y);
             l0 = __fadd2_rn(l0, y0);
             l1 = __fadd2_rn(l1, y1);
@@ -342,9 +381,18 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             p[i / 2 + 1] = pack16<INT8>(y1.x, y1.y);
           }
           tmem_st32_async(s_addr + 32 * q, p);
+          if (q == 0) {
+            // the first half of the weights' product starts under the second half's exponentials
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(phalf0 + 8 * t);
+          }
         }
         l += (l0.x + l0.y) + (l1.x + l1.y);
         tmem_wait_st();
+      } else if (lane == 0) {
+        mbar_arrive(phalf0 + 8 * t);
       }
       tc_fence_before();
       __syncwarp();
@@ -356,27 +404,28 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       tc_fence_after();
       const int64_t tok = sq.start + (there ? row / group : 0);
       const int h = g * group + (int)(there ? row % group : 0);
-      const bool none = nt[t] == 0;
-      const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+      const bool none = lim <= 0;              // no cache row to see here
+      const float inv = none ? 0.0f : 1.0f / l;
       const int64_t at = ((int64_t)split * a.tokens + tok) * a.heads + h;
-      if (P.splits > 1 && there) P.part_ml[at] = make_float2(none || l == 0.0f ? -INFINITY : ref, l);
+      if (P.splits > 1 && there) P.part_ml[at] = none ? make_float2(-INFINITY, 0.0f) : make_float2(ref, l);
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         uint32_t o[32];
+        if (nt[t] > 0) {
+          tmem_ld32_async(o_addr + 32 * q, o);
+          tmem_wait_ld();
+        }
         if (none) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
-        } else {
-          tmem_ld32_async(o_addr + 32 * q, o);
-          tmem_wait_ld();
         }
         if (!there) continue;
         if (P.splits == 1) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + (int64_t)h * D + 32 * q);
           uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)       // (a row that sees nothing has no sum: its output is 0)
-            w[i] = l == 0.0f ? 0u : pack16<false>(f_of(o[2 * i]) * inv, f_of(o[2 * i + 1]) * inv);
+          for (int i = 0; i < 16; ++i)
+            w[i] = pack16<false>(f_of(o[2 * i]) * inv, f_of(o[2 * i + 1]) * inv);
 #pragma unroll
           for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         } else {
@@ -392,48 +441,59 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     fewer_registers<T::R_PRODUCT>();
     if (warp == 8) {
     // ================================================================= products
-    if (lane == 0 && n > 0) {
+    const int un = (int)warp_uniform((uint32_t)n), unt[2] = {(int)warp_uniform((uint32_t)nt[0]), (int)warp_uniform((uint32_t)nt[1])};
+    const uint32_t utm = warp_uniform(tmem);
+    const bool utail = !INT8 && warp_any(tail);
+    if (un > 0) {
+      const uint32_t elected = elect_lane();
       const uint32_t ID_S = idesc_f16(INT8, KT, false), ID_O = idesc_f16(INT8, D, true);
       auto scores = [&](int t, int slot) {
         const uint32_t q = sbase + T::Q_OFF + t * T::TILE, k = sbase + T::KV_OFF + slot * T::TILE;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
-          mma_ss(tmem + 128 * t, operand_desc(q + (s >> 2) * T::HALF + 32 * (s & 3)),
-                 operand_desc(k + (s >> 2) * T::HALF + 32 * (s & 3)), ID_S, s > 0);
-        mma_commit(sfull0 + 8 * t);
+          mma_ss(utm + 128 * t, operand_desc(q + (s >> 2) * T::HALF + 32 * (s & 3)),
+                 operand_desc(k + (s >> 2) * T::HALF + 32 * (s & 3)), ID_S, s > 0, elected);
+        mma_commit_if(elected, sfull0 + 8 * t);
       };
-      auto outputs = [&](int t, int slot, bool first) {
+      auto outputs = [&](int t, int slot, bool first, int half) {
         const uint32_t v = sbase + T::KV_OFF + slot * T::TILE;
 #pragma unroll
-        for (int s = 0; s < KT / 16; ++s)
-          mma_ts(tmem + T::O_COL + D * t, tmem + 128 * t + 8 * s, v_desc(v + 2048 * s), ID_O, !first || s > 0);
+        for (int s = half * KT / 32; s < (half + 1) * KT / 32; ++s)
+          mma_ts(utm + T::O_COL + D * t, utm + 128 * t + 8 * s, v_desc(v + 2048 * s), ID_O, !first || s > 0, elected);
       };
-      bool ok = mbar_wait(qready, 0) && mbar_wait(full0, 0) && !*fail;
+      bool ok = mbar_wait_warp(qready, 0) && mbar_wait_warp(full0, 0) && !warp_any(*fail);
       if (ok) {
         tc_fence_after();
+#pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (nt[t] > 0) scores(t, 0);
-        mma_commit(empty0);
+          if (unt[t] > 0) scores(t, 0);
+        mma_commit_if(elected, empty0);
       }
-      for (int j = 0; j < n && ok; ++j) {
+      for (int j = 0; j < un && ok; ++j) {
         const int vi = 2 * j + 1, ki = 2 * j + 2;
         const int vslot = vi % SLOTS, kslot = ki % SLOTS;
         bool v_here = false, k_here = false;
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (j < nt[t]) {
-            ok = mbar_wait(pready0 + 8 * t, (uint32_t)j & 1u) && !*fail;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok) break;
+          if (j < unt[t]) {
+            ok = mbar_wait_warp(phalf0 + 8 * t, (uint32_t)j & 1u) && !warp_any(*fail);
             if (ok && !v_here) {
-              ok = mbar_wait(full0 + 8 * vslot, (uint32_t)(vi / SLOTS) & 1u) && !*fail;
-              if (ok && !INT8 && tail && j == n - 1) ok = mbar_wait(vtail, 0) && !*fail;
+              ok = mbar_wait_warp(full0 + 8 * vslot, (uint32_t)(vi / SLOTS) & 1u) && !warp_any(*fail);
+              if (ok && utail && j == un - 1) ok = mbar_wait_warp(vtail, 0) && !warp_any(*fail);
               v_here = true;
             }
             if (!ok) break;
             tc_fence_after();
-            outputs(t, vslot, j == 0);
-            if (j == nt[t] - 1) mma_commit(ofull0 + 8 * t);
+            outputs(t, vslot, j == 0, 0);
+            ok = mbar_wait_warp(pready0 + 8 * t, (uint32_t)j & 1u) && !warp_any(*fail);
+            if (!ok) break;
+            tc_fence_after();
+            outputs(t, vslot, j == 0, 1);
+            if (j == unt[t] - 1) mma_commit_if(elected, ofull0 + 8 * t);
           }
-          if (j + 1 < nt[t]) {
-            if (!k_here) ok = mbar_wait(full0 + 8 * kslot, (uint32_t)(ki / SLOTS) & 1u) && !*fail;
+          if (j + 1 < unt[t]) {
+            if (!k_here) ok = mbar_wait_warp(full0 + 8 * kslot, (uint32_t)(ki / SLOTS) & 1u) && !warp_any(*fail);
             k_here = true;
             if (!ok) break;
             tc_fence_after();
@@ -441,56 +501,64 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           }
         }
         if (!ok) break;
-        mma_commit(empty0 + 8 * vslot);
-        if (j + 1 < n) mma_commit(empty0 + 8 * kslot);
+        mma_commit_if(elected, empty0 + 8 * vslot);
+        if (j + 1 < un) mma_commit_if(elected, empty0 + 8 * kslot);
       }
       if (!ok) *fail = 1;
     }
-    } else if (!INT8 && warp == 9) {
+    } else if (warp == 9) {
     // ================================================================= pages by TMA
-    const int box = C.page_size < KT ? C.page_size : KT;
-    const int boxes = KT / box;
+    // bf16: to the K and V slots; INT8: to the code slots. A page's rows of a tile per lane; the
+    // next tile's page numbers are fetched ahead.
+    constexpr int RING = INT8 ? T::RAW_SLOTS : SLOTS;
+    const uint32_t rfull = INT8 ? rawfull0 : full0, rempty = INT8 ? rawempty0 : empty0;
+    const int lg = __ffs(C.page_size) - 1, lbox = lg < 7 ? lg : 7, box = 1 << lbox;
     const int* table = a.page_table + b * a.table_stride;
+    auto page_of = [&](int j) {                      // -1: no row of the sequence
+      const int key = (int)kb + j * KT + (lane << lbox);
+      return (lane << lbox) < KT && j < n && key < sq.len ? __ldg(table + (key >> lg)) : -1;
+    };
+    auto in_tile = [&](int j) { return min(KT >> lbox, (sq.len - (int)kb - j * KT + box - 1) >> lbox); };
     bool ok = true;
-    int i = 0;
-    for (; i < 2 * n && ok; ++i) {
-      const int slot = i % SLOTS;
-      const int64_t key0 = kb + (int64_t)(i >> 1) * KT;
-      const uint32_t bar = full0 + 8 * slot;
-      // pages with a row of the sequence (rows past them keep what was there)
-      const int live = min(boxes, (int)((sq.len - key0 + box - 1) / box));
-      int page = 0;
-      if (lane < live) {
-        page = __ldg(table + (key0 + lane * box) / C.page_size);
-        if (page < 0 || page >= C.pages) {
-          atomicOr(A.err_word, ERRBIT_BADARG);
-          page = (int)C.pages;                      // outside the map: zeros
+    int i = 0, next = page_of(0);
+    for (int j = 0; j < n && ok; ++j) {
+      const int live = in_tile(j), prow = ((int)kb + j * KT + (lane << lbox)) & (C.page_size - 1);
+      int page = next;
+      next = page_of(j + 1);
+      if (lane < live && (page < 0 || page >= C.pages)) {
+        atomicOr(A.err_word, ERRBIT_BADARG);
+        page = (int)C.pages;                        // outside the map: zeros
+      }
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int slot = i % RING;
+        const uint32_t bar = rfull + 8 * slot;
+        if (!mbar_wait_warp(rempty + 8 * slot, ((uint32_t)(i / RING) & 1u) ^ 1u) || warp_any(*fail)) {
+          ok = false;
+          break;
         }
-      }
-      int got = 1;
-      if (lane == 0) {
-        got = mbar_wait(empty0 + 8 * slot, ((uint32_t)(i / SLOTS) & 1u) ^ 1u) && !*fail;
-        if (got) mbar_expect_tx(bar, (uint32_t)live * box * D * 2);
-      }
-      ok = __shfl_sync(FULL, got, 0) != 0;
-      if (ok && lane < live) {
-        const uint32_t dst = sbase + T::KV_OFF + slot * T::TILE + lane * box * 128;
-        const int prow = (int)((key0 + lane * box) % C.page_size);
-        for (int h = 0; h < D / 64; ++h)
-          tma_load_4d(dst + h * T::HALF, (i & 1) ? &tmV : &tmK, 64 * h, prow, g, page, bar);
+        // (rows of pages past the sequence keep what was there)
+        if (lane == 0) mbar_expect_tx(bar, (uint32_t)live * box * D * (INT8 ? 1 : 2));
+        __syncwarp();
+        if (lane < live) {
+          const CUtensorMap* map = kv ? &tmV : &tmK;
+          if constexpr (INT8) {
+            tma_load_4d(sbase + T::RAW_OFF + slot * T::RAW + (lane << lbox) * D, map, 0, prow, g, page, bar);
+          } else {
+            const uint32_t dst = sbase + T::KV_OFF + slot * T::TILE + (lane << lbox) * 128;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) tma_load_4d(dst + h * T::HALF, map, 64 * h, prow, g, page, bar);
+          }
+        }
+        ++i;
       }
     }
-    if (!ok) {
-      *fail = 1;
-      --i;                                           // this tile's copies were not issued
-    }
-    // zeros for the values past the sequence, which may be anything (0 * NaN)
-    if (ok && tail && n > 0) {
-      const int li = 2 * n - 1, slot = li % SLOTS;
-      int got = 1;
-      if (lane == 0) got = mbar_wait(full0 + 8 * slot, (uint32_t)(li / SLOTS) & 1u) && !*fail;
-      if (__shfl_sync(FULL, got, 0)) {
-        const int valid = (int)(sq.len - (kb + (int64_t)(n - 1) * KT));
+    if (!ok) *fail = 1;
+    // bf16: zeros for the values past the sequence, which may be anything (0 * NaN)
+    if (!INT8 && ok && tail && n > 0) {
+      const int slot = (i - 1) % RING;
+      if (mbar_wait_warp(rfull + 8 * slot, (uint32_t)((i - 1) / RING) & 1u)) {
+        const int valid = sq.len - (int)kb - (n - 1) * KT;
         for (int e = valid * 8 + lane; e < KT * 8; e += 32)
           for (int h = 0; h < D / 64; ++h)
             *reinterpret_cast<uint4*>(base + T::KV_OFF + slot * T::TILE + h * T::HALF + e * 16) = make_uint4(0, 0, 0, 0);
@@ -503,83 +571,65 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     }
     // on failure, copies in flight land before the CTA ends
     if (*fail && lane == 0)
-      for (int k = i > SLOTS ? i - SLOTS : 0; k < i; ++k)
-        mbar_wait(full0 + 8 * (k % SLOTS), (uint32_t)(k / SLOTS) & 1u);
+      for (int k = i > RING ? i - RING : 0; k < i; ++k)
+        mbar_wait(rfull + 8 * (k % RING), (uint32_t)(k / RING) & 1u);
     }
   } else if constexpr (INT8) {
     fewer_registers<T::R_CONVERT>();
     // ================================================================= codes to fp16
     constexpr int CPR = D / 16, RPP = 128 / CPR, ROUNDS = KT / RPP;   // 16 codes per thread and round
     const int w = tid - 12 * 32, ch = w % CPR, r0 = w / CPR;
+    const int lg = __ffs(C.page_size) - 1;
     const int* table = a.page_table + b * a.table_stride;
-    uint4 next[ROUNDS];
     float nks = 0.0f, nvs = 0.0f;
-    auto page_at = [&](int64_t key) -> int64_t {      // -1: no such row
-      if (key >= sq.len) return -1;
-      const int page = __ldg(table + key / C.page_size);
-      if (page < 0 || page >= C.pages) {
-        atomicOr(A.err_word, ERRBIT_BADARG);
-        return -1;
-      }
-      return page;
-    };
-    auto fetch = [&](int i) {
-      const int64_t key0 = kb + (int64_t)(i >> 1) * KT;
-      const int8_t* src = static_cast<const int8_t*>((i & 1) ? C.v : C.k);
-#pragma unroll
-      for (int x = 0; x < ROUNDS; ++x) {
-        const int64_t key = key0 + r0 + x * RPP;
-        const int64_t page = page_at(key);
-        next[x] = make_uint4(0, 0, 0, 0);
-        if (page >= 0)
-          next[x] = __ldg(reinterpret_cast<const uint4*>(src + page * C.page_stride + (int64_t)g * C.head_stride +
-                                                         (key % C.page_size) * C.row_stride) + ch);
-      }
-      if (!(i & 1)) {
-        const int64_t key = key0 + w, page = page_at(key);
-        nks = nvs = 0.0f;
-        if (page >= 0) {
-          const int64_t at = (page * G + g) * C.page_size + key % C.page_size;
-          nks = __ldg(C.k_scales + at);
-          nvs = __ldg(C.v_scales + at);
-        }
-      }
+    auto fetch_scales = [&](int j) {                 // of row w of tile j; 0 past the sequence
+      const int key = (int)kb + j * KT + w;
+      nks = nvs = 0.0f;
+      if (j >= n || key >= sq.len) return;
+      const int page = __ldg(table + (key >> lg));
+      if (page < 0 || page >= C.pages) return;       // (the loader reports it)
+      const int64_t at = ((int64_t)page * G + g) * C.page_size + (key & (C.page_size - 1));
+      nks = __ldg(C.k_scales + at);
+      nvs = __ldg(C.v_scales + at);
     };
     bool ok = true;
-    if (n > 0) fetch(0);
+    fetch_scales(0);
     for (int i = 0; i < 2 * n && ok; ++i) {
-      const int slot = i % SLOTS;
-      uint4 cur[ROUNDS];
-#pragma unroll
-      for (int x = 0; x < ROUNDS; ++x) cur[x] = next[x];
-      const float cks = nks, cvs = nvs;
-      if (i + 1 < 2 * n) fetch(i + 1);
-      ok = mbar_wait(empty0 + 8 * slot, ((uint32_t)(i / SLOTS) & 1u) ^ 1u) && !*fail;
+      const int slot = i % SLOTS, rslot = i % T::RAW_SLOTS, j = i >> 1;
+      ok = mbar_wait(rawfull0 + 8 * rslot, (uint32_t)(i / T::RAW_SLOTS) & 1u) && !*fail;
+      ok = ok && mbar_wait(empty0 + 8 * slot, ((uint32_t)(i / SLOTS) & 1u) ^ 1u) && !*fail;
       if (!ok) break;
+      const int valid = sq.len - (int)kb - j * KT;   // rows past them may be anything: zeros
+      const uint4* src = reinterpret_cast<const uint4*>(base + T::RAW_OFF + rslot * T::RAW);
       unsigned char* tile = base + T::KV_OFF + slot * T::TILE + (ch >> 2) * T::HALF;
 #pragma unroll
       for (int x = 0; x < ROUNDS; ++x) {
         const int r = r0 + x * RPP;
-        const uint32_t u[4] = {cur[x].x ^ 0x80808080u, cur[x].y ^ 0x80808080u, cur[x].z ^ 0x80808080u, cur[x].w ^ 0x80808080u};
+        uint4 v = src[r * CPR + ch];
+        if (r >= valid) v = make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
         uint4* row = reinterpret_cast<uint4*>(tile + r * 128);
         row[(2 * (ch & 3)) ^ (r & 7)] = make_uint4(codes_lo_f16(u[0]), codes_hi_f16(u[0]), codes_lo_f16(u[1]), codes_hi_f16(u[1]));
         row[(2 * (ch & 3) + 1) ^ (r & 7)] = make_uint4(codes_lo_f16(u[2]), codes_hi_f16(u[2]), codes_lo_f16(u[3]), codes_hi_f16(u[3]));
       }
       if (!(i & 1)) {
-        // the scales of tile j outlive its K slot: four sets, the fourth next one is written only
-        // after both softmaxes have passed this one
-        const int j = i >> 1;
+        // four sets of scales: the set's last readers, the softmaxes of tile j - 4, are done when the
+        // products of tile j - 2 have freed this slot
         float* sc = reinterpret_cast<float*>(base + T::SC_OFF) + (j & 3) * 2 * KT;
-        sc[w] = cks;
-        sc[KT + w] = cvs;
-        float mx = cvs;
+        sc[w] = nks;
+        sc[KT + w] = nvs;
+        float mx = nvs;
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
         if (lane == 0) reinterpret_cast<float*>(base + T::SC_OFF + 4 * 2 * KT * 4)[(j & 3) * 4 + w / 32] = mx;
+        fetch_scales(j + 1);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(full0 + 8 * slot);
+      if (lane == 0) {
+        mbar_arrive(rawempty0 + 8 * rslot);
+        mbar_arrive(full0 + 8 * slot);
+      }
     }
     if (!ok) *fail = 1;
   }
@@ -594,17 +644,20 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   }
 }
 
-// [pages][kv_heads][page_size][head_dim] bf16 with the cache's strides, box of 64 channels x (at
-// most 128) rows, 128-byte swizzle, zeros outside
+// [pages][kv_heads][page_size][head_dim] with the cache's strides, boxes of (at most 128) rows: bf16, 64
+// channels with the 128-byte swizzle; INT8, whole rows as they are. Zeros outside.
 bool cache_map(CUtensorMap* map, const dq_kv_cache& C, const void* p) {
   EncodeTiledFn fn = encoder();
   if (fn == nullptr) return false;
+  const bool q8 = C.kind == DQ_CACHE_INT8;
+  const cuuint64_t es = q8 ? 1 : 2;
   const cuuint64_t dims[4] = {(cuuint64_t)C.head_dim, (cuuint64_t)C.page_size, (cuuint64_t)C.kv_heads, (cuuint64_t)C.pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)C.row_stride * 2, (cuuint64_t)C.head_stride * 2, (cuuint64_t)C.page_stride * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)std::min(C.page_size, KT), 1, 1};
+  const cuuint64_t strides[3] = {C.row_stride * es, C.head_stride * es, C.page_stride * es};
+  const cuuint32_t box[4] = {q8 ? (cuuint32_t)C.head_dim : 64, (cuuint32_t)std::min(C.page_size, KT), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(map, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -615,7 +668,7 @@ cudaError_t launch_kind(const AttnArgs& A, const AttnPlan& P, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
   if (e != cudaSuccess) return e;
   alignas(64) CUtensorMap tk = {}, tv = {};
-  if (!INT8 && (!cache_map(&tk, A.cache, A.cache.k) || !cache_map(&tv, A.cache, A.cache.v)))
+  if (!cache_map(&tk, A.cache, A.cache.k) || !cache_map(&tv, A.cache, A.cache.v))
     return cudaErrorInvalidValue;
   const int64_t x = P.splits * A.cache.kv_heads * P.row_tiles;
   if (x > INT32_MAX) return cudaErrorInvalidConfiguration;

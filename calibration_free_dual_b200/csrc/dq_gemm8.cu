@@ -6,7 +6,7 @@
 // make a narrow tile instead of an idle one, and the epilogue's lanes run along a row of y.
 //   * warp 0 (one lane): per slice of 128 channels, one TMA tile load of either operand (128-byte
 //     swizzle) on the slice's "full" mbarrier;
-//   * warp 1 (one lane): four MMAs per slice, committed to the slice's "empty" mbarrier;
+//   * warp 1: four MMAs per slice, committed to the slice's "empty" mbarrier;
 //   * warps 2-5: the accumulator, converted and scaled, to y.
 // Every wait is bounded; on timeout the kernel raises the error word, frees its TMEM and returns.
 #include <algorithm>
@@ -31,12 +31,12 @@ __host__ __device__ constexpr uint32_t idesc_i8(int m, int n) {
 }
 
 __device__ __forceinline__ void mma_i8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                       uint32_t idesc, uint32_t accumulate) {
+                                       uint32_t idesc, uint32_t accumulate, uint32_t elected) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected) : "memory");
 }
 
 template <int BN>
@@ -103,11 +103,12 @@ gemm8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
     if (*fail)                                     // copies still in flight land before the CTA ends
       for (int j = k > C::STAGES ? k - C::STAGES : 0; j < k; ++j)
         mbar_wait(full0 + 8 * (j % C::STAGES), (uint32_t)(j / C::STAGES) & 1u);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
+    const uint32_t elected = elect_lane(), acc = warp_uniform(tmem);
     bool ok = true;
     for (int k = 0; k < nk; ++k) {
       const int s = k % C::STAGES;
-      if (!mbar_wait(full0 + 8 * s, (uint32_t)(k / C::STAGES) & 1u) || *fail) {
+      if (!mbar_wait_warp(full0 + 8 * s, (uint32_t)(k / C::STAGES) & 1u) || warp_any(*fail)) {
         *fail = 1;
         ok = false;
         break;
@@ -116,11 +117,11 @@ gemm8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
       const uint32_t st = sbase + s * C::STAGE;
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb)
-        mma_i8(tmem, operand_desc(st + 32 * kb), operand_desc(st + C::A_BYTES + 32 * kb),
-               idesc_i8(BM, BN), (k > 0 || kb > 0) ? 1u : 0u);
-      mma_commit(empty0 + 8 * s);
+        mma_i8(acc, operand_desc(st + 32 * kb), operand_desc(st + C::A_BYTES + 32 * kb),
+               idesc_i8(BM, BN), (k > 0 || kb > 0) ? 1u : 0u, elected);
+      mma_commit_if(elected, empty0 + 8 * s);
     }
-    if (ok) mma_commit(accbar);
+    if (ok) mma_commit_if(elected, accbar);
   } else if (warp >= 2) {
     const int sp = warp & 3;
     const int64_t n = n0 + sp * 32 + lane;

@@ -45,13 +45,15 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes)
                : "memory");
 }
+// one try, which suspends the thread up to about 10 ms (0x989680 ns) while the phase is open: polls would
+// take shared-memory bandwidth from the tensor core's operands
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+      : "=r"(ok) : "r"(bar), "r"(parity), "r"(0x989680u) : "memory");
   return ok != 0;
 }
 __device__ __forceinline__ uint64_t global_ns() {
@@ -59,8 +61,13 @@ __device__ __forceinline__ uint64_t global_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// bounded wait for the phase with the given parity to complete; false after WAIT_LIMIT_NS
+// bounded wait for the phase with the given parity to complete; false after WAIT_LIMIT_NS. The first
+// tries (each suspends the thread for a while) go without the global timer, whose read takes longer
+// than most waits.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   while (!mbar_try(bar, parity))
     if (global_ns() - t0 > WAIT_LIMIT_NS) return false;
@@ -165,6 +172,38 @@ inline EncodeTiledFn encoder() {
       fn = reinterpret_cast<EncodeTiledFn>(p);
   }
   return fn;
+}
+
+// ---- issue by a whole warp. The instructions of the tensor core take descriptors and addresses from
+// uniform registers. A loop run by one lane, or one whose branches the compiler cannot see to be the
+// same for all lanes, moves them there one by one, about 100 clocks a product; so the issuing warp
+// runs its loop with all lanes, its waits and flags reduced over the warp, and one elected lane
+// executes each instruction by predicate.
+__device__ __forceinline__ bool warp_any(bool p) { return __any_sync(0xFFFFFFFFu, p) != 0; }
+__device__ __forceinline__ uint32_t warp_uniform(uint32_t v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
+// mbar_wait for a converged warp, with a uniform result
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (warp_any(mbar_try(bar, parity))) return true;
+  const uint64_t t0 = global_ns();
+#pragma unroll 1
+  while (!warp_any(mbar_try(bar, parity)))
+    if (warp_any(global_ns() - t0 > WAIT_LIMIT_NS)) return false;
+  return true;
+}
+// one lane of the converged warp, by predicate
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_commit_if(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      :: "r"(bar), "r"(elected) : "memory");
 }
 
 inline int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }

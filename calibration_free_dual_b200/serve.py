@@ -8,7 +8,6 @@ outputs then belong to that stream until it has been waited for.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -16,56 +15,58 @@ import torch
 from . import _lib
 from .api import DQError, _check, _dtype_code, _need_cuda
 
-_NULL = contextlib.nullcontext()
+# A decode step's kernels take a few microseconds, so the helpers are written for few Python
+# operations a call: conditions are tested in line, and what is wrong is worked out only when
+# one of them fails; the stream is read as a raw handle, and results are allocated by strides.
+_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_alloc = torch.empty_strided
 
 
 def _place(t: torch.Tensor, stream):
     """The context (device, stream) in which a call on `t` allocates and launches."""
-    if stream is not None:
-        if stream.device != t.device:
-            raise ValueError("stream and tensors are on different devices")
-        return torch.cuda.stream(stream)           # also makes the stream's device current
-    if t.device.index != torch.cuda.current_device():
+    if stream is None:
         return torch.cuda.device(t.device)
-    return _NULL
+    if stream.device != t.device:
+        raise ValueError("stream and tensors are on different devices")
+    return torch.cuda.stream(stream)               # also makes the stream's device current
 
 
-def _cur(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
-
-
-def _same(t, like: torch.Tensor, name: str, dtype) -> None:
-    _need_cuda(t, name)
-    if t.device != like.device:
-        raise ValueError(name + " is on another device")
-    if t.dtype != dtype:
+def _expect(t, dev: int, name: str, dtype) -> None:
+    """A CUDA tensor of the call's device and the given dtype."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype):
+        _need_cuda(t, name)
+        if t.get_device() != dev:
+            raise ValueError(name + " is on another device")
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
 
 
-def _vector(t, like: torch.Tensor, name: str, n: int, dtype) -> None:
-    _same(t, like, name, dtype)
-    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+def _vector(t, dev: int, name: str, n: int, dtype) -> int:
+    """Address of a contiguous vector of n entries."""
+    _expect(t, dev, name, dtype)
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError("%s must be contiguous with %d entries" % (name, n))
+    return t.data_ptr()
 
 
 def _scratch(workspace, need: int, like: torch.Tensor) -> torch.Tensor:
     if workspace is None:
-        return torch.empty((need,), dtype=torch.uint8, device=like.device)
-    _same(workspace, like, "workspace", torch.uint8)
+        return _alloc((need,), (1,), dtype=torch.uint8, device=like.device)
+    _expect(workspace, like.get_device(), "workspace", torch.uint8)
     if not workspace.is_contiguous() or workspace.numel() < need:
         raise ValueError("workspace needs %d contiguous bytes" % need)
     return workspace
 
 
-def _rows_of(X: torch.Tensor, name: str) -> None:
-    _need_cuda(X, name)
-    if X.dim() != 2 or (X.stride(1) != 1 and X.numel() > 0):
+def _rows_of(X: torch.Tensor, name: str):
+    """(rows, columns, row pitch) of a 2-D row-major tensor. A single row's stride carries no
+    meaning and may be anything."""
+    if X.dim() != 2:
         raise ValueError(name + " must be 2-D row-major")
-
-
-def _pitch(t: torch.Tensor) -> int:
-    # (a single row's stride carries no meaning and may be anything)
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+    (T, n), (pitch, one) = X.shape, X.stride()
+    if one != 1 and n > 1 and T > 0:
+        raise ValueError(name + " must be 2-D row-major")
+    return T, n, (pitch if T > 1 else n)
 
 
 def row_quant(X: torch.Tensor, c: torch.Tensor | None = None, stream=None,
@@ -74,68 +75,78 @@ def row_quant(X: torch.Tensor, c: torch.Tensor | None = None, stream=None,
 
     Activations: X [tokens, channels] with the solver's c. Weights: X [out, in] with 1 / c.
     Returns {"codes": int8 [rows, n], "scales": fp32 [rows]} (written into `out` if given)."""
-    _rows_of(X, "X")
+    _need_cuda(X, "X")
+    dev = X.get_device()
+    if stream is not None or dev != _device():
+        with _place(X, stream):
+            return row_quant(X, c, None, out)
+    T, n, pitch = _rows_of(X, "X")
     dt = _dtype_code(X)
-    T, n = X.shape
-    if c is not None:
-        _vector(c, X, "c", n, torch.float32)
-    with _place(X, stream):
-        if out is None:
-            out = dict(codes=torch.empty((T, n), dtype=torch.int8, device=X.device),
-                       scales=torch.empty((T,), dtype=torch.float32, device=X.device))
-        else:
-            _codes_of(out, X, "out")
-            if tuple(out["codes"].shape) != (T, n):
-                raise ValueError("out has another shape than X")
-        _check(_lib.get().dq_row_quant(X.data_ptr(), dt, T, n, _pitch(X),
-                                       None if c is None else c.data_ptr(),
-                                       out["codes"].data_ptr(), out["scales"].data_ptr(),
-                                       _cur(X)), "dq_row_quant")
+    cp = None if c is None else _vector(c, dev, "c", n, torch.float32)
+    if out is None:
+        out = {"codes": _alloc((T, n), (n, 1), dtype=torch.int8, device=X.device),
+               "scales": _alloc((T,), (1,), dtype=torch.float32, device=X.device)}
+        q, s = out["codes"].data_ptr(), out["scales"].data_ptr()
+    else:
+        rows, cols, q, s = _codes_of(out, dev, "out")
+        if rows != T or cols != n:
+            raise ValueError("out has another shape than X")
+    st = _lib.get().dq_row_quant(X.data_ptr(), dt, T, n, pitch, cp, q, s, _raw_stream(dev))
+    if st:
+        _check(st, "dq_row_quant")
     return out
 
 
-def _codes_of(d: dict, like: torch.Tensor, name: str):
-    q, s = d["codes"], d["scales"]
-    _same(q, like, name + " codes", torch.int8)
+def _codes_of(d: dict, dev: int, name: str):
+    """(rows, columns, address of the codes, address of the scales)"""
+    q = d["codes"]
+    _expect(q, dev, name + " codes", torch.int8)
     if q.dim() != 2 or not q.is_contiguous():
         raise ValueError(name + " codes must be 2-D and contiguous")
-    _vector(s, like, name + " scales", q.shape[0], torch.float32)
-    return q, s
+    T, K = q.shape
+    return T, K, q.data_ptr(), _vector(d["scales"], dev, name + " scales", T, torch.float32)
 
 
-def _result(out, T: int, N: int, dtype, like: torch.Tensor) -> torch.Tensor:
-    if dtype not in (torch.float32, torch.bfloat16):
+def _result(out, T: int, N: int, dtype, like: torch.Tensor):
+    """(tensor, dtype code, row pitch) of a product's result."""
+    if dtype is torch.float32:
+        code = _lib.DQ_F32
+    elif dtype is torch.bfloat16:
+        code = _lib.DQ_BF16
+    else:
         raise TypeError("out_dtype must be float32 or bfloat16")
     if out is None:
-        return torch.empty((T, N), dtype=dtype, device=like.device)
-    _same(out, like, "out", dtype)
-    if tuple(out.shape) != (T, N) or (out.stride(1) != 1 and N > 1):
-        raise ValueError("out must be [%d, %d], row-major" % (T, N))
-    return out
+        return _alloc((T, N), (N, 1), dtype=dtype, device=like.device), code, N
+    _expect(out, like.get_device(), "out", dtype)
+    if tuple(out.shape) != (T, N):
+        raise ValueError("out must be [%d, %d]" % (T, N))
+    return out, code, _rows_of(out, "out")[2]
 
 
 def w8a8_gemm(x: dict, w: dict, out_dtype=torch.float32, stream=None,
               workspace: torch.Tensor | None = None,
               out: torch.Tensor | None = None) -> torch.Tensor:
     """dq_w8a8_gemm: y[T, N] from two row_quant results, x (tokens) and w (output channels)."""
-    xq = x["codes"]
-    _need_cuda(xq, "x codes")
-    xq, xs = _codes_of(x, xq, "x")
-    wq, ws = _codes_of(w, xq, "w")
-    T, K = xq.shape
-    N = wq.shape[0]
-    if wq.shape[1] != K:
+    xt = x["codes"]
+    _need_cuda(xt, "x codes")
+    dev = xt.get_device()
+    if stream is not None or dev != _device():
+        with _place(xt, stream):
+            return w8a8_gemm(x, w, out_dtype, None, workspace, out)
+    T, K, xq, xs = _codes_of(x, dev, "x")
+    N, Kw, wq, ws = _codes_of(w, dev, "w")
+    if Kw != K:
         raise ValueError("activation and weight K differ")
     lib = _lib.get()
     need = lib.dq_w8a8_gemm_workspace_bytes(T, N, K)
     if need == 0:
         raise DQError(_lib.DQ_ERR_SHAPE, "K must be a multiple of 16 up to 131072")
-    with _place(xq, stream):
-        y = _result(out, T, N, out_dtype, xq)
-        sp = _scratch(workspace, need, xq)
-        _check(lib.dq_w8a8_gemm(xq.data_ptr(), xs.data_ptr(), T, wq.data_ptr(), ws.data_ptr(),
-                                N, K, y.data_ptr(), _dtype_code(y), _pitch(y), sp.data_ptr(),
-                                sp.numel(), _cur(xq)), "dq_w8a8_gemm")
+    y, code, pitch = _result(out, T, N, out_dtype, xt)
+    sp = _scratch(workspace, need, xt)
+    st = lib.dq_w8a8_gemm(xq, xs, T, wq, ws, N, K, y.data_ptr(), code, pitch, sp.data_ptr(),
+                          sp.numel(), _raw_stream(dev))
+    if st:
+        _check(st, "dq_w8a8_gemm")
     return y
 
 
@@ -143,26 +154,27 @@ def w8a8_linear(X: torch.Tensor, w: dict, c: torch.Tensor | None = None,
                 out_dtype=torch.bfloat16, stream=None, workspace: torch.Tensor | None = None,
                 out: torch.Tensor | None = None) -> torch.Tensor:
     """dq_w8a8_linear: y[T, N] = row_quant(X, c) times an 8-bit weight `w`."""
-    _rows_of(X, "X")
+    _need_cuda(X, "X")
+    dev = X.get_device()
+    if stream is not None or dev != _device():
+        with _place(X, stream):
+            return w8a8_linear(X, w, c, out_dtype, None, workspace, out)
+    T, K, pitch = _rows_of(X, "X")
     dt = _dtype_code(X)
-    wq, ws = _codes_of(w, X, "w")
-    T, K = X.shape
-    N = wq.shape[0]
-    if wq.shape[1] != K:
+    N, Kw, wq, ws = _codes_of(w, dev, "w")
+    if Kw != K:
         raise ValueError("activation and weight K differ")
-    if c is not None:
-        _vector(c, X, "c", K, torch.float32)
+    cp = None if c is None else _vector(c, dev, "c", K, torch.float32)
     lib = _lib.get()
     need = lib.dq_w8a8_linear_workspace_bytes(T, N, K)
     if need == 0:
         raise DQError(_lib.DQ_ERR_SHAPE, "K must be a multiple of 16 up to 131072")
-    with _place(X, stream):
-        y = _result(out, T, N, out_dtype, X)
-        sp = _scratch(workspace, need, X)
-        _check(lib.dq_w8a8_linear(X.data_ptr(), dt, T, K, _pitch(X),
-                                  None if c is None else c.data_ptr(), wq.data_ptr(),
-                                  ws.data_ptr(), N, y.data_ptr(), _dtype_code(y), _pitch(y),
-                                  sp.data_ptr(), sp.numel(), _cur(X)), "dq_w8a8_linear")
+    y, code, ypitch = _result(out, T, N, out_dtype, X)
+    sp = _scratch(workspace, need, X)
+    st = lib.dq_w8a8_linear(X.data_ptr(), dt, T, K, pitch, cp, wq, ws, N, y.data_ptr(), code,
+                            ypitch, sp.data_ptr(), sp.numel(), _raw_stream(dev))
+    if st:
+        _check(st, "dq_w8a8_linear")
     return y
 
 
@@ -187,36 +199,46 @@ def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, dtype=tor
     return d
 
 
-def _cache_of(cache: dict, like: torch.Tensor) -> _lib.dq_kv_cache:
+def _cache_of(cache: dict, dev: int) -> _lib.dq_kv_cache:
     k, v = cache["k"], cache["v"]
-    if k.dtype not in CACHE_TYPES:
-        raise TypeError("the cache must be bfloat16 or int8, got %s" % k.dtype)
-    _same(k, like, "cache k", k.dtype)
-    _same(v, like, "cache v", k.dtype)
-    if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or k.stride(3) != 1:
+    dtype = getattr(k, "dtype", None)
+    if dtype not in CACHE_TYPES:
+        raise TypeError("the cache must be bfloat16 or int8, got %s" % dtype)
+    _expect(k, dev, "cache k", dtype)
+    _expect(v, dev, "cache v", dtype)
+    shape, strides = k.shape, k.stride()
+    if len(shape) != 4 or v.shape != shape or v.stride() != strides or strides[3] != 1:
         raise ValueError("cache k and v must be [pages, kv_heads, page_size, head_dim] with the "
                          "same strides and contiguous channels")
-    P, G, S, D = k.shape
-    # (the stride of an axis of one entry carries no meaning)
-    ps, hs, rs = (s if n > 1 else S * G * D for s, n in zip(k.stride()[:3], (P, G, S)))
-    scales = (None, None)
-    if k.dtype == torch.int8:
-        for name in ("k_scales", "v_scales"):
-            _same(cache[name], like, "cache " + name, torch.float32)
-            if tuple(cache[name].shape) != (P, G, S) or not cache[name].is_contiguous():
-                raise ValueError("cache %s must be contiguous [pages, kv_heads, page_size]" % name)
-        scales = (cache["k_scales"].data_ptr(), cache["v_scales"].data_ptr())
-    return _lib.dq_kv_cache(CACHE_TYPES[k.dtype], S, D, G, P, k.data_ptr(), v.data_ptr(), ps, hs,
-                            rs, *scales)
+    P, G, S, D = shape
+    ps, hs, rs, _ = strides
+    # the stride of an axis of one entry carries no meaning
+    if P == 1:
+        ps = G * S * D
+    if G == 1:
+        hs = S * D
+    if dtype is torch.bfloat16:
+        return _lib.dq_kv_cache(_lib.DQ_CACHE_BF16, S, D, G, P, k.data_ptr(), v.data_ptr(), ps,
+                                hs, rs, None, None)
+    ks, vs = cache["k_scales"], cache["v_scales"]
+    for t, name in ((ks, "cache k_scales"), (vs, "cache v_scales")):
+        _expect(t, dev, name, torch.float32)
+        if t.shape != shape[:3] or not t.is_contiguous():
+            raise ValueError(name + " must be contiguous [pages, kv_heads, page_size]")
+    return _lib.dq_kv_cache(_lib.DQ_CACHE_INT8, S, D, G, P, k.data_ptr(), v.data_ptr(), ps, hs,
+                            rs, ks.data_ptr(), vs.data_ptr())
 
 
-def _heads(x: torch.Tensor, name: str, T: int, D: int) -> int:
-    """Token stride of [T, heads, D] with contiguous heads."""
-    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D:
+def _heads(x: torch.Tensor, name: str, T: int, D: int):
+    """(heads, token stride) of [T, heads, D] with contiguous heads."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != D:
         raise ValueError("%s must be [%d, heads, %d]" % (name, T, D))
-    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != D)):
+    H = shape[1]
+    t, h, d = x.stride()
+    if T > 0 and (d != 1 or (H > 1 and h != D)):
         raise ValueError("%s must have contiguous heads and channels" % name)
-    return x.stride(0) if T > 1 else x.shape[1] * D
+    return H, (t if T > 1 else H * D)
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: dict, slots: torch.Tensor,
@@ -228,41 +250,52 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: dict, slots: torch.Tensor
     cos, sin [rows, dim / 2] (fp32) where these are given. With q [T, heads, head_dim], returns
     the rotated queries in bfloat16 (in `q_out` if given, which may be q)."""
     _need_cuda(k, "k")
+    dev = k.get_device()
+    if stream is not None or dev != _device():
+        with _place(k, stream):
+            return kv_append(k, v, cache, slots, positions, cos, sin, q, interleaved, q_out)
     dt = _dtype_code(k)
-    _same(v, k, "v", k.dtype)
-    c = _cache_of(cache, k)
-    T, D, G = k.shape[0], c.head_dim, c.kv_heads
-    ks, vs = _heads(k, "k", T, D), _heads(v, "v", T, D)
-    if k.dim() != 3 or k.shape[1] != G or v.shape[1] != G:
+    _expect(v, dev, "v", k.dtype)
+    c = _cache_of(cache, dev)
+    T, D, G = k.shape[0] if k.dim() else 0, c.head_dim, c.kv_heads
+    kh, ks = _heads(k, "k", T, D)
+    vh, vs = _heads(v, "v", T, D)
+    if kh != G or vh != G:
         raise ValueError("k and v must have the cache's %d heads" % G)
-    _vector(slots, k, "slots", T, torch.int64)
+    sp = _vector(slots, dev, "slots", T, torch.int64)
     rot = None
     if positions is not None or cos is not None or sin is not None:
         if positions is None or cos is None or sin is None:
             raise ValueError("positions, cos and sin go together")
-        _vector(positions, k, "positions", T, torch.int32)
-        for t, name in ((cos, "cos"), (sin, "sin")):
-            _same(t, k, name, torch.float32)
-            if t.dim() != 2 or not t.is_contiguous() or t.shape != cos.shape:
-                raise ValueError("cos and sin must be contiguous [rows, dim / 2]")
-        rot = _lib.dq_rotary(cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), cos.shape[0],
-                             2 * cos.shape[1], int(bool(interleaved)))
-    with _place(k, stream):
-        qa = (None, 0, 0, None, 0)
-        if q is not None:
-            _same(q, k, "q", k.dtype)
-            qs, H = _heads(q, "q", T, D), q.shape[1]
-            if q_out is None:
-                q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=k.device)
-            _same(q_out, k, "q_out", torch.bfloat16)
+        pp = _vector(positions, dev, "positions", T, torch.int32)
+        _expect(cos, dev, "cos", torch.float32)
+        _expect(sin, dev, "sin", torch.float32)
+        if cos.dim() != 2 or sin.shape != cos.shape or not (cos.is_contiguous()
+                                                            and sin.is_contiguous()):
+            raise ValueError("cos and sin must be contiguous [rows, dim / 2]")
+        rows, half = cos.shape
+        rot = ctypes.byref(_lib.dq_rotary(cos.data_ptr(), sin.data_ptr(), pp, rows, 2 * half,
+                                          1 if interleaved else 0))
+    qp = op = None
+    H = qs = os = 0
+    if q is not None:
+        _expect(q, dev, "q", k.dtype)
+        H, qs = _heads(q, "q", T, D)
+        if q_out is None:
+            os = H * D
+            q_out = _alloc((T, H, D), (os, D, 1), dtype=torch.bfloat16, device=k.device)
+        else:
+            _expect(q_out, dev, "q_out", torch.bfloat16)
             if q_out.shape != q.shape:
                 raise ValueError("q_out must have q's shape")
-            qa = (q.data_ptr(), qs, H, q_out.data_ptr(), _heads(q_out, "q_out", T, D))
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        _check(_lib.get().dq_kv_append(
-            ctypes.byref(c), T, dt, k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(),
-            None if rot is None else ctypes.byref(rot), *qa, _cur(k)), "dq_kv_append")
+            os = _heads(q_out, "q_out", T, D)[1]
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    st = _lib.get().dq_kv_append(ctypes.byref(c), T, dt, k.data_ptr(), ks, v.data_ptr(), vs, sp,
+                                 rot, qp, qs, H, op, os, _raw_stream(dev))
+    if st:
+        _check(st, "dq_kv_append")
     return q_out
 
 
@@ -278,44 +311,55 @@ def paged_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor,
     width): tight bounds make the launch plan fit. Rows of `out` that belong to no sequence are
     left as they are."""
     _need_cuda(q, "q")
-    if q.dtype != torch.bfloat16:
+    dev = q.get_device()
+    if stream is not None or dev != _device():
+        with _place(q, stream):
+            return paged_attention(q, cache, page_table, lengths, q_starts, max_q, max_len,
+                                   causal, scale, out, None, workspace)
+    if q.dtype is not torch.bfloat16:
         raise TypeError("q must be bfloat16, got %s" % q.dtype)
-    c = _cache_of(cache, q)
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, heads, head_dim]")
-    T, H, D = q.shape[0], q.shape[1], c.head_dim
-    qs = _heads(q, "q", T, D)
-    _same(page_table, q, "page_table", torch.int32)
-    if page_table.dim() != 2 or (page_table.numel() and page_table.stride(1) != 1
-                                 and page_table.shape[1] > 1):
+    c = _cache_of(cache, dev)
+    T, D = q.shape[0] if q.dim() else 0, c.head_dim
+    H, qs = _heads(q, "q", T, D)
+    _expect(page_table, dev, "page_table", torch.int32)
+    if page_table.dim() != 2:
         raise ValueError("page_table must be 2-D row-major")
     B, width = page_table.shape
-    _vector(lengths, q, "lengths", B, torch.int32)
+    pitch, one = page_table.stride()
+    if one != 1 and width > 1 and B > 0:
+        raise ValueError("page_table must be 2-D row-major")
+    if B <= 1:
+        pitch = width
+    lp = _vector(lengths, dev, "lengths", B, torch.int32)
+    sp = None
     if q_starts is not None:
-        _vector(q_starts, q, "q_starts", B + 1, torch.int32)
+        sp = _vector(q_starts, dev, "q_starts", B + 1, torch.int32)
     elif T != B:
         raise ValueError("without q_starts there is one token per sequence")
     if max_q is None:
-        max_q = T if q_starts is not None else min(T, 1)
+        max_q = T if sp is not None else 1
+    if max_q > T:
+        max_q = T
     if max_len is None:
         max_len = width * c.page_size
     elif max_len > width * c.page_size:
         raise ValueError("max_len is more than the page table's width holds")
-    with _place(q, stream):
-        if out is None:
-            out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
-        else:
-            _same(out, q, "out", torch.bfloat16)
-            if out.shape != q.shape:
-                raise ValueError("out must have q's shape")
-        a = _lib.dq_attention(q.data_ptr(), out.data_ptr(), qs, _heads(out, "out", T, D), T, B, H,
-                              int(bool(causal)), None if q_starts is None else q_starts.data_ptr(),
-                              lengths.data_ptr(), page_table.data_ptr(),
-                              page_table.stride(0) if B > 1 else width, min(max_q, T), max_len,
-                              D ** -0.5 if scale is None else scale)
-        lib = _lib.get()
-        need = lib.dq_paged_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(a))
-        sp = _scratch(workspace, max(need, 16), q)
-        _check(lib.dq_paged_attention(ctypes.byref(c), ctypes.byref(a), sp.data_ptr(), sp.numel(),
-                                      _cur(q)), "dq_paged_attention")
+    if out is None:
+        os = H * D
+        out = _alloc((T, H, D), (os, D, 1), dtype=torch.bfloat16, device=q.device)
+    else:
+        _expect(out, dev, "out", torch.bfloat16)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        os = _heads(out, "out", T, D)[1]
+    a = _lib.dq_attention(q.data_ptr(), out.data_ptr(), qs, os, T, B, H, 1 if causal else 0, sp,
+                          lp, page_table.data_ptr(), pitch, max_q, max_len,
+                          D ** -0.5 if scale is None else scale)
+    lib = _lib.get()
+    cr, ar = ctypes.byref(c), ctypes.byref(a)
+    need = lib.dq_paged_attention_workspace_bytes(cr, ar)
+    ws = _scratch(workspace, need if need > 16 else 16, q)
+    st = lib.dq_paged_attention(cr, ar, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if st:
+        _check(st, "dq_paged_attention")
     return out
