@@ -2,13 +2,19 @@
 // y[t, i] = fl32(fl32(sum_j x[t, j] w[i, j]) * fl32(xs[t] * ws[i])), the integer sum exact.
 //
 // sm_100a design: tcgen05.mma.kind::i8 (32 channels per instruction, int32 accumulators in tensor
-// memory). The weight rows are the MMA's 128 rows and the tokens its columns, so that few tokens
-// make a narrow tile instead of an idle one, and the epilogue's lanes run along a row of y.
-//   * warp 0 (one lane): per slice of 128 channels, one TMA tile load of either operand (128-byte
-//     swizzle) on the slice's "full" mbarrier;
-//   * warp 1: four MMAs per slice, committed to the slice's "empty" mbarrier;
-//   * warps 2-5: the accumulator, converted and scaled, to y.
-// Every wait is bounded; on timeout the kernel raises the error word, frees its TMEM and returns.
+// memory). The weight rows are the MMA's rows and the tokens its columns, so that few tokens make a
+// narrow tile instead of an idle one, and the epilogue's lanes run along a row of y. Slices of 128
+// channels arrive by TMA (128-byte swizzle) in a ring. By warps: 0 loads, 1 issues the products, 2-5
+// convert, scale and write. Two kernels:
+//   * pair: two CTAs on two SMs share a tile of 256 weight rows x up to 256 tokens (cta_group::2): each
+//     loads its own 128 weight rows and half of the tokens, so a tile's operands cross from L2 once for
+//     both and the tensor core's shared-memory reads stay below its rate. Persistent, with two
+//     accumulators in turn, so that a tile's epilogue runs under the next one's products;
+//   * split: for few tiles (few tokens, or a small weight). One CTA per 128 weight rows x 32 to 256 tokens
+//     and all or part of K; the parts of a tile form a cluster and add their int32 sums through distributed
+//     shared memory (exact, so the split does not show in the result).
+// Every wait on an mbarrier is bounded; on timeout the kernel raises the error word, frees its TMEM
+// and returns.
 #include <algorithm>
 #include <cstring>
 
@@ -22,7 +28,8 @@ namespace {
 
 constexpr unsigned FULL_MASK = 0xFFFFFFFFu;
 constexpr int GT = 192;
-constexpr int BM = 128;                 // weight rows of a tile
+constexpr int BM = 128;                 // weight rows of a CTA
+constexpr int BN_MAX = 256;             // tokens of a tile, at most
 constexpr int BK = 128;                 // channels (bytes) of a slice
 
 // A, B signed 8-bit, D int32, both operands K-major
@@ -30,96 +37,139 @@ __host__ __device__ constexpr uint32_t idesc_i8(int m, int n) {
   return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+template <int CTAS>
 __device__ __forceinline__ void mma_i8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                        uint32_t idesc, uint32_t accumulate, uint32_t elected) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected) : "memory");
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected) : "memory");
 }
 
-template <int BN>
-struct Cfg {
-  static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 128 ? 3 : 5;
-  static constexpr int BAR = STAGES * STAGE;
-  static constexpr int SMEM = BAR + 256 + 1024;
-  static constexpr uint32_t COLS = BN < 32 ? 32 : BN;
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// a shared-memory address of this CTA, as the same place in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ int4 ld_cluster4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// one result (rounded once more for bf16)
+template <bool BF16OUT>
+__device__ __forceinline__ void put(void* y, int64_t at, int acc, float scale) {
+  const float v = __fmul_rn(__int2float_rn(acc), scale);
+  if (BF16OUT) static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
+  else static_cast<float*>(y)[at] = v;
+}
+
+// ------------------------------------------------------------------------------------ split
+// Plan of a launch: `bn` tokens a tile; split kernel: `parts` CTAs of `per` slices each
+struct Plan8 {
+  bool pair;
+  int bn, parts, per, stages, smem;
+  int64_t row_tiles, tok_tiles;
 };
 
-template <int BN, bool BF16OUT>
+constexpr int SPLIT_STAGES_MAX = 8;
+constexpr int PARTS_MAX = 8;             // CTAs of a cluster
+
+template <bool BF16OUT>
 __global__ void __launch_bounds__(GT)
-gemm8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-             const Gemm8Args A) {
-  using C = Cfg<BN>;
+gemm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const Gemm8Args A, const Plan8 P) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * SPLIT_STAGES_MAX + 1];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int fail;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t n0 = (int64_t)blockIdx.x * BM, t0 = (int64_t)blockIdx.y * BN;
+  const int part = (int)(blockIdx.x % P.parts);
+  const int64_t n0 = (int64_t)(blockIdx.x / P.parts) * BM, t0 = (int64_t)blockIdx.y * P.bn;
+  const int stages = P.stages, stage = BM * BK + P.bn * BK;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
-  unsigned char* base_ptr = smem_raw + (sbase - raw);
-  const uint32_t full0 = sbase + C::BAR, empty0 = full0 + 8 * C::STAGES;
-  const uint32_t accbar = empty0 + 8 * C::STAGES;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::BAR + 8 * (2 * C::STAGES + 1));
-  volatile int* fail = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* red = reinterpret_cast<int*>(smem_raw + (sbase - raw));   // [tokens][128 weight rows], after the products
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * SPLIT_STAGES_MAX, accbar = empty0 + 8 * SPLIT_STAGES_MAX;
+  const uint32_t cols = P.bn <= 32 ? 32u : P.bn <= 64 ? 64u : P.bn <= 128 ? 128u : 256u;
 
-  if (warp == 0) tmem_alloc(smem_u32(tmem_slot), C::COLS);
+  if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), cols);
   if (tid == 32) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
     mbar_init(accbar, 1);
-    *fail = 0;
+    fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int nk = (int)((A.K + BK - 1) / BK);
+  const uint32_t tmem = tmem_slot;
+  const int slices = (int)((A.K + BK - 1) / BK);
+  const int k0 = part * P.per, nk = min(P.per, slices - k0);      // at least one slice each
 
   if (warp == 0 && lane == 0) {
     // the weight does not depend on the quantizer's launch: its first slices go ahead
-    const int head = nk < C::STAGES ? nk : C::STAGES;
+    const int head = min(nk, stages);
     for (int k = 0; k < head; ++k) {
-      mbar_expect_tx(full0 + 8 * k, C::STAGE);
-      tma_load_2d(sbase + k * C::STAGE, &tmW, k * BK, (int)n0, full0 + 8 * k);
+      mbar_expect_tx(full0 + 8 * k, stage);
+      tma_load_2d(sbase + k * stage, &tmW, (k0 + k) * BK, (int)n0, full0 + 8 * k);
     }
     if (A.after_rows) asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int k = 0; k < head; ++k)
-      tma_load_2d(sbase + k * C::STAGE + C::A_BYTES, &tmX, k * BK, (int)t0, full0 + 8 * k);
-    int k = head;
+      tma_load_2d(sbase + k * stage + BM * BK, &tmX, (k0 + k) * BK, (int)t0, full0 + 8 * k);
+    int k = head, s = 0;
+    uint32_t par = 0;
     for (; k < nk; ++k) {
-      const int s = k % C::STAGES;
-      if (!mbar_wait(empty0 + 8 * s, ((uint32_t)(k / C::STAGES) & 1u) ^ 1u)) { *fail = 1; break; }
-      if (*fail) break;
-      const uint32_t st = sbase + s * C::STAGE;
-      mbar_expect_tx(full0 + 8 * s, C::STAGE);
-      tma_load_2d(st, &tmW, k * BK, (int)n0, full0 + 8 * s);
-      tma_load_2d(st + C::A_BYTES, &tmX, k * BK, (int)t0, full0 + 8 * s);
+      if (!mbar_wait(empty0 + 8 * s, par) || fail) { fail = 1; break; }
+      mbar_expect_tx(full0 + 8 * s, stage);
+      tma_load_2d(sbase + s * stage, &tmW, (k0 + k) * BK, (int)n0, full0 + 8 * s);
+      tma_load_2d(sbase + s * stage + BM * BK, &tmX, (k0 + k) * BK, (int)t0, full0 + 8 * s);
+      if (++s == stages) { s = 0; par ^= 1u; }
     }
-    if (*fail)                                     // copies still in flight land before the CTA ends
-      for (int j = k > C::STAGES ? k - C::STAGES : 0; j < k; ++j)
-        mbar_wait(full0 + 8 * (j % C::STAGES), (uint32_t)(j / C::STAGES) & 1u);
+    if (fail)                                      // copies still in flight land before the CTA ends
+      for (int j = k > stages ? k - stages : 0; j < k; ++j)
+        mbar_wait(full0 + 8 * (j % stages), (uint32_t)(j / stages) & 1u);
   } else if (warp == 1) {
-    const uint32_t elected = elect_lane(), acc = warp_uniform(tmem);
+    const uint32_t elected = elect_lane(), acc = warp_uniform(tmem), idesc = idesc_i8(BM, P.bn);
     bool ok = true;
+    int s = 0;
+    uint32_t par = 0;
     for (int k = 0; k < nk; ++k) {
-      const int s = k % C::STAGES;
-      if (!mbar_wait_warp(full0 + 8 * s, (uint32_t)(k / C::STAGES) & 1u) || warp_any(*fail)) {
-        *fail = 1;
+      if (!mbar_wait_warp(full0 + 8 * s, par) || warp_any(fail)) {
+        fail = 1;
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t st = sbase + s * C::STAGE;
+      const uint32_t st = sbase + s * stage;
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb)
-        mma_i8(acc, operand_desc(st + 32 * kb), operand_desc(st + C::A_BYTES + 32 * kb),
-               idesc_i8(BM, BN), (k > 0 || kb > 0) ? 1u : 0u, elected);
+        mma_i8<1>(acc, operand_desc(st + 32 * kb), operand_desc(st + BM * BK + 32 * kb), idesc,
+                  (k > 0 || kb > 0) ? 1u : 0u, elected);
       mma_commit_if(elected, empty0 + 8 * s);
+      if (++s == stages) { s = 0; par ^= 1u; }
     }
     if (ok) mma_commit_if(elected, accbar);
   } else if (warp >= 2) {
@@ -127,39 +177,251 @@ gemm8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
     const int64_t n = n0 + sp * 32 + lane;
     const float wsc = n < A.N ? __ldg(A.ws + n) : 0.0f;
     if (A.after_rows) asm volatile("griddepcontrol.wait;" ::: "memory");
-    int got = 0;
-    if (lane == 0) got = (mbar_wait(accbar, 0) && !*fail) ? 1 : 0;
-    if (__shfl_sync(FULL_MASK, got, 0)) {
+    const int cnt = (int)(A.T - t0 < P.bn ? A.T - t0 : P.bn);
+    if (mbar_wait_warp(accbar, 0) && !warp_any(fail)) {
       tc_fence_after();
-      const int cols = (int)(A.T - t0 < BN ? A.T - t0 : BN);
 #pragma unroll 1
-      for (int cb = 0; cb < cols; cb += 32) {
+      for (int cb = 0; cb < cnt; cb += 32) {
         float v[32];
         tmem_ld32(tmem + ((uint32_t)(sp * 32) << 16) + cb, v);
-        const float xsc = cb + lane < cols ? A.xs[t0 + cb + lane] : 0.0f;
+        if (P.parts > 1) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float y = __fmul_rn(__int2float_rn(__float_as_int(v[j])),
-                                    __fmul_rn(__shfl_sync(FULL_MASK, xsc, j), wsc));
-          if (cb + j < cols && n < A.N) {
-            const int64_t at = (t0 + cb + j) * A.ldy + n;
-            if (BF16OUT) static_cast<__nv_bfloat16*>(A.y)[at] = __float2bfloat16_rn(y);
-            else static_cast<float*>(A.y)[at] = y;
+          for (int j = 0; j < 32; ++j)
+            red[(cb + j) * BM + sp * 32 + lane] = __float_as_int(v[j]);
+        } else {
+          const float xsc = cb + lane < cnt ? A.xs[t0 + cb + lane] : 0.0f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float sc = __fmul_rn(__shfl_sync(FULL_MASK, xsc, j), wsc);
+            if (cb + j < cnt && n < A.N)
+              put<BF16OUT>(A.y, (t0 + cb + j) * A.ldy + n, __float_as_int(v[j]), sc);
           }
         }
       }
-    } else if (lane == 0) {
-      *fail = 1;
+    } else {
+      fail = 1;
     }
   }
-
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *fail) atomicOr(A.err_word, ERRBIT_TIMEOUT);
+  if (P.parts > 1) {
+    // ---- add the parts: each CTA a strip of the tile's weight rows
+    cluster_sync();
+    const bool good = fail == 0;
+    if (A.after_rows) asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int cnt = (int)(A.T - t0 < P.bn ? A.T - t0 : P.bn);
+    const uint32_t mine = smem_u32(red);
+    if (good) {
+      // (strips of whole groups of four rows, loaded 16 bytes at a time, all parts in flight)
+      constexpr int QUADS = BM / 4;
+      const int lo = part * QUADS / P.parts, width = (part + 1) * QUADS / P.parts - lo;
+      uint32_t peer[PARTS_MAX];
+#pragma unroll
+      for (int q = 0; q < PARTS_MAX; ++q) peer[q] = map_rank(mine, q < P.parts ? q : 0);
+      for (int e = tid; e < cnt * width; e += GT) {
+        const int t = e / width, r = 4 * (lo + e - t * width);
+        const uint32_t off = 4u * (uint32_t)(t * BM + r);
+        int4 v[PARTS_MAX];
+#pragma unroll
+        for (int q = 0; q < PARTS_MAX; ++q) v[q] = q < P.parts ? ld_cluster4(peer[q] + off) : make_int4(0, 0, 0, 0);
+        int4 sum = v[0];
+#pragma unroll
+        for (int q = 1; q < PARTS_MAX; ++q) {
+          sum.x += v[q].x; sum.y += v[q].y; sum.z += v[q].z; sum.w += v[q].w;
+        }
+        const float xsc = A.xs[t0 + t];
+        const int64_t at = (t0 + t) * A.ldy + n0 + r;
+        const int sums[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n0 + r + i < A.N) put<BF16OUT>(A.y, at + i, sums[i], __fmul_rn(xsc, __ldg(A.ws + n0 + r + i)));
+      }
+    }
+    cluster_sync();                                  // the sums have been read
+  }
+  if (tid == 0 && fail) atomicOr(A.err_word, ERRBIT_TIMEOUT);
   if (warp == 0) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, C::COLS);
+    tmem_dealloc(tmem, cols);
+  }
+}
+
+// ------------------------------------------------------------------------------------- pair
+constexpr int PAIR_STAGES = 6;
+constexpr int PAIR_STAGE = 2 * BM * BK;             // 128 weight rows, up to 128 token rows
+constexpr int PAIR_SMEM = PAIR_STAGES * PAIR_STAGE + 1024;
+
+// a TMA tile load that completes on an mbarrier of the pair's first CTA
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// completes when all products issued so far have, on the barrier of that place in both CTAs
+__device__ __forceinline__ void commit_pair(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}"
+      :: "r"(bar), "r"(elected), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+
+// tile index -> weight and token tile: 8 token tiles wide, so that the tiles in flight share operands
+__device__ __forceinline__ void tile_at(int64_t idx, const Plan8& P, int64_t& nt, int64_t& tt) {
+  constexpr int64_t WIDE = 8;
+  const int64_t per = WIDE * P.row_tiles, g = idx / per, in = idx % per;
+  const int64_t w = P.tok_tiles - g * WIDE < WIDE ? P.tok_tiles - g * WIDE : WIDE;
+  nt = in / w;
+  tt = g * WIDE + in % w;
+}
+
+template <bool BF16OUT>
+__global__ void __launch_bounds__(GT, 1)
+gemm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                  const Gemm8Args A, const Plan8 P) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * PAIR_STAGES + 4];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int fail;
+  __shared__ __align__(16) float xs_s[4][BN_MAX];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * PAIR_STAGES;
+  const uint32_t accfull0 = empty0 + 8 * PAIR_STAGES, accempty0 = accfull0 + 16;
+  const uint32_t lead_full0 = map_rank(full0, 0), lead_accempty0 = map_rank(accempty0, 0);
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(&tmem_slot)), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (tid == 32) {
+    for (int s = 0; s < PAIR_STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accfull0 + 8 * b, 1);
+      mbar_init(accempty0 + 8 * b, 8);              // four warps of either CTA
+    }
+    fail = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int nk = (int)((A.K + BK - 1) / BK);
+  const int64_t tiles = P.row_tiles * P.tok_tiles, first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int half = P.bn / 2;                         // token rows of either CTA
+
+  if (warp == 0 && lane == 0) {
+    const uint32_t bytes = 2u * (uint32_t)(BM + half) * BK;        // of both CTAs
+    int s = 0, issued = 0;
+    uint32_t par = 1;
+    bool ok = true, waited = !A.after_rows;
+    for (int64_t idx = first; idx < tiles && ok; idx += step) {
+      int64_t nt, tt;
+      tile_at(idx, P, nt, tt);
+      const int n0 = (int)(nt * 2 * BM + rank * BM), t0 = (int)(tt * P.bn + rank * half);
+      for (int k = 0; k < nk; ++k) {
+        if (!mbar_wait(empty0 + 8 * s, par) || fail) { ok = false; break; }
+        const uint32_t st = sbase + s * PAIR_STAGE, bar = lead_full0 + 8 * s;
+        if (rank == 0) mbar_expect_tx(full0 + 8 * s, bytes);
+        tma_load_pair(st, &tmW, k * BK, n0, bar);
+        if (!waited) {                               // the codes come from the launch before
+          asm volatile("griddepcontrol.wait;" ::: "memory");
+          waited = true;
+        }
+        tma_load_pair(st + BM * BK, &tmX, k * BK, t0, bar);
+        ++issued;
+        if (++s == PAIR_STAGES) { s = 0; par ^= 1u; }
+      }
+    }
+    if (!ok) {
+      fail = 1;
+      // copies in flight land before the pair ends (the first CTA's barriers count both CTAs')
+      if (rank == 0)
+        for (int j = issued > PAIR_STAGES ? issued - PAIR_STAGES : 0; j < issued; ++j)
+          mbar_wait(full0 + 8 * (j % PAIR_STAGES), (uint32_t)(j / PAIR_STAGES) & 1u);
+    }
+  } else if (warp == 1 && rank == 0) {
+    const uint32_t elected = elect_lane(), acc = warp_uniform(tmem), idesc = idesc_i8(2 * BM, P.bn);
+    int s = 0, it = 0;
+    uint32_t par = 0;
+    bool ok = true;
+    for (int64_t idx = first; idx < tiles && ok; idx += step, ++it) {
+      const int b = it & 1;
+      ok = mbar_wait_warp(accempty0 + 8 * b, ((uint32_t)(it >> 1) & 1u) ^ 1u);
+      if (!ok) break;
+      tc_fence_after();
+      for (int k = 0; k < nk; ++k) {
+        if (!mbar_wait_warp(full0 + 8 * s, par) || warp_any(fail)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t st = sbase + s * PAIR_STAGE;
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb)
+          mma_i8<2>(acc + BN_MAX * b, operand_desc(st + 32 * kb), operand_desc(st + BM * BK + 32 * kb), idesc,
+                    (k > 0 || kb > 0) ? 1u : 0u, elected);
+        commit_pair(elected, empty0 + 8 * s);
+        if (++s == PAIR_STAGES) { s = 0; par ^= 1u; }
+      }
+      if (ok) commit_pair(elected, accfull0 + 8 * b);
+    }
+    if (!ok) fail = 1;
+  } else if (warp >= 2) {
+    const int sp = warp & 3;
+    if (A.after_rows) asm volatile("griddepcontrol.wait;" ::: "memory");
+    int it = 0;
+    for (int64_t idx = first; idx < tiles; idx += step, ++it) {
+      const int b = it & 1;
+      int64_t nt, tt;
+      tile_at(idx, P, nt, tt);
+      const int64_t n = nt * 2 * BM + rank * BM + sp * 32 + lane, t0 = tt * P.bn;
+      const int cnt = (int)(A.T - t0 < P.bn ? A.T - t0 : P.bn);
+      const float wsc = n < A.N ? __ldg(A.ws + n) : 0.0f;
+      __syncwarp();
+      for (int j = lane; j < cnt; j += 32) xs_s[sp][j] = A.xs[t0 + j];
+      __syncwarp();
+      if (!mbar_wait_warp(accfull0 + 8 * b, (uint32_t)(it >> 1) & 1u)) { fail = 1; break; }
+      tc_fence_after();
+#pragma unroll 1
+      for (int cb = 0; cb < cnt; cb += 32) {
+        float v[32];
+        tmem_ld32(tmem + ((uint32_t)(sp * 32) << 16) + BN_MAX * b + cb, v);
+        if (n < A.N) {
+          const int64_t at = (t0 + cb) * A.ldy + n;
+          if (cnt - cb >= 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              put<BF16OUT>(A.y, at + j * A.ldy, __float_as_int(v[j]), __fmul_rn(xs_s[sp][cb + j], wsc));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < cnt - cb)
+                put<BF16OUT>(A.y, at + j * A.ldy, __float_as_int(v[j]), __fmul_rn(xs_s[sp][cb + j], wsc));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(lead_accempty0 + 8 * b);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                                    // both CTAs are done with either's memory
+  if (tid == 0 && fail) atomicOr(A.err_word, ERRBIT_TIMEOUT);
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512u) : "memory");
   }
 }
 
@@ -176,42 +438,111 @@ bool codes8_map(CUtensorMap* map, const int8_t* codes, int64_t rows, int64_t K, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool BF16OUT>
-cudaError_t launch_tile(const Gemm8Args& A, cudaStream_t s) {
-  using C = Cfg<BN>;
-  alignas(64) CUtensorMap tw, tx;
-  if (!codes8_map(&tw, A.w, A.N, A.K, BM) || !codes8_map(&tx, A.x, A.T, A.K, BN))
-    return cudaErrorInvalidValue;
-  constexpr auto K = gemm8_kernel<BN, BF16OUT>;
-  cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((A.N + BM - 1) / BM), (unsigned)((A.T + BN - 1) / BN));
-  cfg.blockDim = dim3(GT);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = A.after_rows ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, K, tw, tx, A);
-  count_launches(1);
-  return e;
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The plan with the least estimated time, in clocks of an SM: products at the measured rates (a product
+// of 32 channels takes max(tokens / 2, 32 + tokens / 4)), operands at 40 bytes a clock and SM from
+// L2, a weight that is hardly reused at 28 (HBM; 22 where an SM holds one CTA; 3400 for all SMs), what a
+// CTA spends besides, and the sum of split tiles.
+Plan8 plan_gemm8(int64_t T, int64_t N, int64_t K) {
+  const int64_t slices = ceil_div(K, BK), hbm = N * K / 3400;
+  Plan8 best = {};
+  int64_t best_cost = INT64_MAX;
+  for (int bn = 64; bn <= BN_MAX; bn += 32) {
+    Plan8 P = {};
+    P.pair = true;
+    P.bn = bn;
+    P.row_tiles = ceil_div(N, 2 * BM);
+    P.tok_tiles = ceil_div(T, bn);
+    const int64_t rounds = ceil_div(P.row_tiles * P.tok_tiles, SERVE_SMS / 2);
+    const int64_t slice = std::max<int64_t>(2 * bn, BM * BK / (P.tok_tiles <= 2 ? 28 : 40) + bn / 2 * BK / 40);
+    const int64_t cost = std::max(rounds * slices * slice, hbm) + 5000 + 10 * bn;
+    if (cost <= best_cost) {
+      best_cost = cost;
+      best = P;
+    }
+  }
+  static const int widths[] = {32, 64, 96, 128, 192, 256};
+  for (const int bn : widths) {
+    for (int parts = 1; parts <= PARTS_MAX && parts <= slices; ++parts) {
+      Plan8 P = {};
+      P.bn = bn;
+      P.per = (int)ceil_div(slices, parts);
+      P.parts = (int)ceil_div(slices, P.per);
+      P.row_tiles = ceil_div(N, BM);
+      P.tok_tiles = ceil_div(T, bn);
+      const int64_t ctas = P.row_tiles * P.tok_tiles * P.parts, hold = bn <= 64 ? 2 : 1;
+      const int64_t per_sm = std::min(hold, ceil_div(ctas, SERVE_SMS));
+      const int64_t waves = ceil_div(ctas, SERVE_SMS * hold);
+      const int64_t slice = per_sm * std::max<int64_t>(4 * std::max(bn / 2, 32 + bn / 4),
+                                                       BM * BK / (P.tok_tiles > 2 ? 40 : per_sm == 1 ? 22 : 28) + bn * BK / 40);
+      const int64_t toks = std::min<int64_t>(T, bn);
+      const int64_t sum = P.parts > 1 ? 1500 + ceil_div(toks * BM / 4, (int64_t)P.parts * GT) * 600 * per_sm : 10 * bn;
+      const int64_t cost = std::max(waves * (P.per * slice + 4000 + sum), hbm + 4000);
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = P;
+      }
+    }
+  }
+  if (!best.pair) {
+    const int stage = (BM + best.bn) * BK;
+    const int budget = (best.bn <= 64 ? 108 : 216) * 1024;      // narrow tiles: two CTAs an SM
+    best.stages = std::min<int>({SPLIT_STAGES_MAX, budget / stage, best.per});
+    const int red = best.parts > 1 ? best.bn * BM * 4 : 0;
+    best.smem = std::max(best.stages * stage, red) + 1024;
+  }
+  return best;
 }
 
-template <int BN>
-cudaError_t launch_out(const Gemm8Args& A, cudaStream_t s) {
-  return A.y_bf16 ? launch_tile<BN, true>(A, s) : launch_tile<BN, false>(A, s);
+cudaError_t launch_cluster(const void* kernel, unsigned x, unsigned y, int smem, int cluster, bool pdl,
+                           cudaStream_t s, void** args) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(x, y);
+  cfg.blockDim = dim3(GT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  e = cudaLaunchKernelExC(&cfg, kernel, args);
+  count_launches(1);
+  return e;
 }
 
 }  // namespace
 
 size_t gemm8_workspace_bytes(int64_t, int64_t, int64_t) { return 16; }
 
-cudaError_t launch_gemm8(const Gemm8Args& A, void*, cudaStream_t s) {
-  if (A.T <= 32) return launch_out<32>(A, s);
-  return launch_out<128>(A, s);
+cudaError_t launch_gemm8(const Gemm8Args& A0, void*, cudaStream_t s) {
+  Gemm8Args A = A0;
+  Plan8 P = plan_gemm8(A.T, A.N, A.K);
+  alignas(64) CUtensorMap tw, tx;
+  if (!codes8_map(&tw, A.w, A.N, A.K, BM) || !codes8_map(&tx, A.x, A.T, A.K, P.pair ? P.bn / 2 : P.bn))
+    return cudaErrorInvalidValue;
+  void* args[] = {&tw, &tx, &A, &P};
+  if (P.pair) {
+    const void* k = A.y_bf16 ? (const void*)gemm8_pair_kernel<true> : (const void*)gemm8_pair_kernel<false>;
+    const int64_t ctas = 2 * std::min<int64_t>(SERVE_SMS / 2, P.row_tiles * P.tok_tiles);
+    return launch_cluster(k, (unsigned)ctas, 1, PAIR_SMEM, 2, A.after_rows, s, args);
+  }
+  const void* k = A.y_bf16 ? (const void*)gemm8_split_kernel<true> : (const void*)gemm8_split_kernel<false>;
+  const int64_t x = P.row_tiles * P.parts;
+  if (x > INT32_MAX || P.tok_tiles > 65535) return cudaErrorInvalidConfiguration;
+  return launch_cluster(k, (unsigned)x, (unsigned)P.tok_tiles, P.smem, P.parts, A.after_rows, s, args);
 }
 
 }  // namespace dq
