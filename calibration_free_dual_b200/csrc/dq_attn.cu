@@ -59,6 +59,20 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
+  const uint2 v = lds8(addr);
+  return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+}
 template <bool F16>
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (F16)
@@ -82,7 +96,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 template <int D, bool INT8>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, INT8 ? 3 : 2)
 attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
   using R = Ring<D, INT8>;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -91,20 +105,18 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
   const dq_attention& a = A.a;
   const dq_kv_cache& C = A.cache;
   const int G = C.kv_heads, group = A.group;
-  const int64_t idx = blockIdx.x;
-  const int split = (int)(idx % P.splits);
-  const int g = (int)(idx / P.splits % G);
-  const int64_t rt = idx / P.splits / G;
+  // (at most 16 rows a key head: one row tile)
+  const unsigned splits = (unsigned)P.splits;
+  const int g = (int)(blockIdx.x / splits), split = (int)(blockIdx.x - g * splits);
   const int b = blockIdx.y;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const SeqBounds sq = seq_bounds(a, b);
-  if (sq.bad && idx == 0 && tid == 0) atomicOr(A.err_word, ERRBIT_BADARG);
-  const int64_t rows = (int64_t)sq.n * group, row0 = rt * 16;
-  if (row0 >= rows) return;
-  const int64_t kb = split * P.chunk;
+  if (sq.bad && blockIdx.x == 0 && tid == 0) atomicOr(A.err_word, ERRBIT_BADARG);
+  const int rows = sq.n * group;
+  if (rows == 0) return;
+  const int kb = split * (int)P.chunk;
   if (split > 0 && kb >= sq.len) return;
-  const int64_t last = row0 + 15 < rows ? row0 + 15 : rows - 1;
-  int64_t ke = min64(sq.len, kb + P.chunk);
-  ke = min64(ke, visible(a, sq, (int)(last / group)));
+  const int ke = min(min(sq.len, kb + (int)P.chunk), visible(a, sq, sq.n - 1));
 
   // this thread's two rows: query pointer, visible cache rows
   const __nv_bfloat16* qp[2];
@@ -112,15 +124,18 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
   bool there[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int64_t r = row0 + rq + 8 * i;
+    const int r = rq + 8 * i;
     there[i] = r < rows;
-    const int64_t t = there[i] ? r / group : 0;
-    lim[i] = there[i] ? visible(a, sq, (int)t) : 0;
-    const int h = g * group + (int)(there[i] ? r % group : 0);
+    const int t = there[i] ? r / group : 0;
+    lim[i] = there[i] ? visible(a, sq, t) : 0;
+    const int h = g * group + (there[i] ? r - t * group : 0);
     qp[i] = static_cast<const __nv_bfloat16*>(a.q) + (sq.start + t) * a.q_stride + (int64_t)h * D;
   }
   // rows that every row of the tile sees need no mask
-  const int64_t all_see = visible(a, sq, (int)(row0 / group));
+  // (a row that is not there needs none either: nothing of it is kept)
+  const int unmasked = min(ke, visible(a, sq, 0));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) lim[i] = min(lim[i], ke);
 
   // Q fragments. bf16: k-step s, pairs at 16 s + 2c and + 8. INT8: the k order within 64 channels is
   // the one in which a thread reads 16 codes of a cache row at once (channel 64u + 16c + 4w + 0..3
@@ -172,41 +187,65 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
     }
   }
 
-  // ---- ring of asynchronous copies
+  // ---- ring of asynchronous copies. A lane's places in a group of 16 rows are fixed: `COPIES` 16-byte
+  // chunks of K and of V, RPC rows apart.
   unsigned char* ring = smem + warp * R::DEPTH * R::SLOT;
-  const int groups = ke > kb ? (int)((ke - kb + KG - 1) / KG) : 0;
+  const int groups = ke > kb ? (ke - kb + KG - 1) / KG : 0;
   const int* table = a.page_table + b * a.table_stride;
-  const int psz = C.page_size;
-  auto page_of = [&](int gi) { return gi < groups ? __ldg(table + (kb + (int64_t)gi * KG) / psz) : 0; };
+  const int lg = __ffs(C.page_size) - 1, first_key = kb;
+  constexpr int COPIES = KG * R::CPR / 32, RPC = 32 / R::CPR, ES = INT8 ? 1 : 2;
+  const int crow = lane / R::CPR, cch = lane % R::CPR;
+  const int64_t row_bytes = C.row_stride * ES, page_bytes = C.page_stride * ES;
+  const int64_t lane_off = (int64_t)g * C.head_stride * ES + crow * row_bytes + cch * 16;
+  const char* kbase = static_cast<const char*>(C.k) + lane_off;
+  const char* vbase = static_cast<const char*>(C.v) + lane_off;
+  const uint32_t ring_addr = smem_addr(ring);
+  uint32_t kdst[COPIES], vdst[COPIES];
+#pragma unroll
+  for (int i = 0; i < COPIES; ++i) {
+    kdst[i] = ring_addr + R::k_chunk(crow + i * RPC, cch) * 16;
+    vdst[i] = ring_addr + KG * R::RB + R::v_chunk(crow + i * RPC, cch) * 16;
+  }
+  auto page_of = [&](int gi) { return gi < groups ? __ldg(table + ((first_key + gi * KG) >> lg)) : 0; };
   int next_page = page_of(warp);
   int issued = warp, slot_w = 0;
   auto issue = [&]() {
     if (issued < groups) {
-      const int64_t key0 = kb + (int64_t)issued * KG;
+      const int key0 = first_key + issued * KG, prow = key0 & (C.page_size - 1);
       int page = next_page;
-      int live = (int)min64(KG, sq.len - key0);          // rows past the length: zeros
-      if (page < 0 || page >= C.pages) {
+      int live = sq.len - key0;                                      // rows past the length: zeros
+      if ((unsigned)page >= (unsigned)C.pages) {
         if (lane == 0) atomicOr(A.err_word, ERRBIT_BADARG);
         page = 0;
         live = 0;
       }
-      const int prow = (int)(key0 % psz);
-      const int64_t at = (int64_t)page * C.page_stride + (int64_t)g * C.head_stride + (int64_t)prow * C.row_stride;
-      const int64_t es = INT8 ? 1 : 2;
-      const uint32_t kd = smem_addr(ring + slot_w * R::SLOT), vd = kd + KG * R::RB;
+      const int64_t at = page * page_bytes + prow * row_bytes;
+      const char* ks = kbase + at;
+      const char* vs = vbase + at;
+      const uint32_t so = slot_w * R::SLOT;
+      if (live >= KG) {
 #pragma unroll
-      for (int i = 0; i < KG * R::CPR / 32; ++i) {
-        const int row = (i * 32 + lane) / R::CPR, ch = lane % R::CPR;
-        const int64_t off = (at + row * C.row_stride) * es + ch * 16;
-        const int bytes = row < live ? 16 : 0;
-        copy16(kd + R::k_chunk(row, ch) * 16, static_cast<const char*>(C.k) + (row < live ? off : 0), bytes);
-        copy16(vd + R::v_chunk(row, ch) * 16, static_cast<const char*>(C.v) + (row < live ? off : 0), bytes);
+        for (int i = 0; i < COPIES; ++i) {
+          copy16(kdst[i] + so, ks, 16);
+          copy16(vdst[i] + so, vs, 16);
+          ks += RPC * row_bytes;
+          vs += RPC * row_bytes;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          const bool in = crow + i * RPC < live;
+          copy16(kdst[i] + so, in ? ks : static_cast<const char*>(C.k), in ? 16 : 0);
+          copy16(vdst[i] + so, in ? vs : static_cast<const char*>(C.v), in ? 16 : 0);
+          ks += RPC * row_bytes;
+          vs += RPC * row_bytes;
+        }
       }
       if (INT8 && lane < 8) {
         const int part = lane & 3;                                   // four scales
-        const float* src = (lane < 4 ? C.k_scales : C.v_scales) + ((int64_t)page * G + g) * psz + prow + 4 * part;
+        const float* src = (lane < 4 ? C.k_scales : C.v_scales) + (((int64_t)page * G + g) << lg) + prow + 4 * part;
         const int bytes = 4 * max(0, min(4, live - 4 * part));
-        copy16(vd + KG * R::RB + lane * 16, bytes > 0 ? src : C.k_scales, bytes);
+        copy16(ring_addr + so + 2 * KG * R::RB + lane * 16, bytes > 0 ? src : C.k_scales, bytes);
       }
       issued += WARPS;
       next_page = page_of(issued);
@@ -219,23 +258,32 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
 
   constexpr int NTL = D / 8;
   float o[NTL][4] = {};
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  float m[2] = {-INFINITY, -INFINITY};
+  float2 l[2] = {};                      // this lane's share of the sums (even and odd columns)
   float vunit = 0x1p-100f;               // INT8: power of two above the values' scales so far
+  float vinv = 0x1p115f;                 // 2^15 / vunit
+  // this lane's places in a slot. bf16: rows of the ldmatrix tiles; INT8: 16 codes of K row rq (half u of
+  // D = 128 swapped by odd rows), D/8 codes of V row 2c
+  const uint32_t k_lane = INT8 ? 0u : (uint32_t)((lane >> 4) * 8 + (lane & 7));
+  const uint32_t v_lane = INT8 ? (uint32_t)(KG * R::RB + (D == 128 ? R::v_chunk(2 * c, rq) * 16 : R::v_chunk(2 * c, rq >> 1) * 16 + 8 * (rq & 1)))
+                               : (uint32_t)(((lane >> 3) & 1) * 8 + (lane & 7));
+  uint32_t k_off[D / 64];
+#pragma unroll
+  for (int u = 0; u < D / 64; ++u) k_off[u] = R::k_chunk(rq, 4 * u + c) * 16;
   int slot_r = 0;
   for (int gi = warp; gi < groups; gi += WARPS) {
     issue();
     asm volatile("cp.async.wait_group %0;" :: "n"(R::DEPTH - 1) : "memory");
     __syncwarp();
-    const unsigned char* kp = ring + slot_r * R::SLOT;
-    const unsigned char* vp = kp + KG * R::RB;
+    const uint32_t kp = ring_addr + slot_r * R::SLOT, vp = kp + KG * R::RB;
     slot_r = slot_r + 1 == R::DEPTH ? 0 : slot_r + 1;
-    // ---- S = Q K^T
+    // ---- S = Q K^T (s[t]: rows rq, rq + 8 of columns 8 t + 2c, + 1)
     float s[2][4] = {};
     if constexpr (!INT8) {
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t kf[4];
-        ldsm4(kf, smem_addr(kp) + R::k_chunk((lane >> 4) * 8 + (lane & 7), 2 * ks + ((lane >> 3) & 1)) * 16);
+        ldsm4(kf, kp + R::k_chunk(k_lane, 2 * ks + ((lane >> 3) & 1)) * 16);
         mma16<false>(s[0], qf[ks], kf[0], kf[1]);
         mma16<false>(s[1], qf[ks], kf[2], kf[3]);
       }
@@ -244,57 +292,70 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int u = 0; u < D / 64; ++u) {
-          const uint4 v = *reinterpret_cast<const uint4*>(kp + R::k_chunk(8 * t + rq, 4 * u + c) * 16);
+          const uint4 v = lds16(kp + k_off[u] + t * 8 * R::RB);
           const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
 #pragma unroll
           for (int i = 0; i < 4; ++i) mma16<true>(s[t], qf[4 * u + i], codes_lo_f16(w[i]), codes_hi_f16(w[i]));
         }
     }
-    float vs[4];
+    // pairs of a row's scores, in log2 units: x[row][t]
+    float2 x[2][2];
+    float2 vs[2];
     if constexpr (INT8) {
-      const float2* scl = reinterpret_cast<const float2*>(vp + KG * R::RB);
-      const float2 k0 = scl[c], k1 = scl[4 + c], v0 = scl[8 + c], v1 = scl[12 + c];
+      const uint32_t scl = vp + KG * R::RB + 8 * c;
+      const float2 k0 = lds_f2(scl), k1 = lds_f2(scl + 32);
+      vs[0] = lds_f2(scl + 64);
+      vs[1] = lds_f2(scl + 96);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        s[0][2 * i] *= k0.x; s[0][2 * i + 1] *= k0.y;
-        s[1][2 * i] *= k1.x; s[1][2 * i + 1] *= k1.y;
+        const float2 s2 = make_float2(sc[i], sc[i]);
+        x[i][0] = mul2(mul2(make_float2(s[0][2 * i], s[0][2 * i + 1]), k0), s2);
+        x[i][1] = mul2(mul2(make_float2(s[1][2 * i], s[1][2 * i + 1]), k1), s2);
       }
-      vs[0] = v0.x; vs[1] = v0.y; vs[2] = v1.x; vs[3] = v1.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          x[i][t] = mul2(make_float2(s[t][2 * i], s[t][2 * i + 1]), make_float2(sc[i], sc[i]));
     }
     // ---- mask, running maximum
-    const int64_t key0 = kb + (int64_t)gi * KG;
-    const bool mask = key0 + KG > all_see || key0 + KG > ke || row0 + 16 > rows;
+    const int key0 = first_key + gi * KG;
+    if (key0 + KG > unmasked) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (key0 + 8 * t + 2 * c >= lim[i]) x[i][t].x = -INFINITY;
+          if (key0 + 8 * t + 2 * c + 1 >= lim[i]) x[i][t].y = -INFINITY;
+        }
+    }
     float top[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float& x = s[t][2 * i + j];
-          x *= sc[i];
-          if (mask && key0 + 8 * t + 2 * c + j >= min64(lim[i], ke)) x = -INFINITY;
-        }
-      top[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+      top[i] = fmaxf(fmaxf(x[i][0].x, x[i][0].y), fmaxf(x[i][1].x, x[i][1].y));
       top[i] = fmaxf(top[i], __shfl_xor_sync(FULL, top[i], 1));
       top[i] = fmaxf(top[i], __shfl_xor_sync(FULL, top[i], 2));
-      top[i] = fmaxf(top[i], m[i]);
     }
     bool grow = top[0] > m[0] || top[1] > m[1];
-    float unit = vunit;
+    float vmax = 0.0f;
     if constexpr (INT8) {
-      float vmax = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
-      vmax = fmaxf(vmax, __shfl_xor_sync(FULL, vmax, 1));
-      vmax = fmaxf(vmax, __shfl_xor_sync(FULL, vmax, 2));
-      if (vmax > vunit && vmax < 0x1p126f) unit = __uint_as_float((__float_as_uint(vmax) & 0x7F800000u) + 0x00800000u);
-      grow = grow || unit > vunit;
+      vmax = fmaxf(fmaxf(vs[0].x, vs[0].y), fmaxf(vs[1].x, vs[1].y));
+      grow = grow || (vmax > vunit && vmax < 0x1p126f);
     }
     if (__any_sync(FULL, grow)) {
+      float unit = vunit;
+      if constexpr (INT8) {
+        vmax = fmaxf(vmax, __shfl_xor_sync(FULL, vmax, 1));
+        vmax = fmaxf(vmax, __shfl_xor_sync(FULL, vmax, 2));
+        if (vmax > vunit && vmax < 0x1p126f) unit = __uint_as_float((__float_as_uint(vmax) & 0x7F800000u) + 0x00800000u);
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        top[i] = fmaxf(top[i], m[i]);
         const float al = top[i] == -INFINITY ? 1.0f : exp2_fast(m[i] - top[i]);
         m[i] = top[i];
-        l[i] *= al;
+        l[i] = mul2(l[i], make_float2(al, al));
         const float ao = INT8 ? al * (vunit / unit) : al;
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
@@ -303,29 +364,26 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
         }
       }
       vunit = unit;
+      vinv = 0x1p15f / unit;
     }
     // ---- P
     uint32_t pf[4];
-    const float vinv = INT8 ? 0x1p15f / vunit : 1.0f;
+    if constexpr (INT8) {
+      const float2 v2 = make_float2(vinv, vinv);
+      vs[0] = mul2(vs[0], v2);
+      vs[1] = mul2(vs[1], v2);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float mm = m[i] == -INFINITY ? 0.0f : m[i];
-      float p[4];
+      const float mm = m[i] == -INFINITY ? 0.0f : -m[i];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) p[2 * t + j] = exp2_fast(s[t][2 * i + j] - mm);
-      if constexpr (INT8) {
-        l[i] += (p[0] + p[1]) + (p[2] + p[3]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] *= vs[j] * vinv;
-        pf[i] = pack2<true>(p[0], p[1]);
-        pf[2 + i] = pack2<true>(p[2], p[3]);
-      } else {
-        // (the sum takes the weights before their rounding)
-        l[i] += (p[0] + p[1]) + (p[2] + p[3]);
-        pf[i] = pack2<false>(p[0], p[1]);
-        pf[2 + i] = pack2<false>(p[2], p[3]);
+      for (int t = 0; t < 2; ++t) {
+        float2 p = __fadd2_rn(x[i][t], make_float2(mm, mm));
+        p.x = exp2_fast(p.x);
+        p.y = exp2_fast(p.y);
+        l[i] = __fadd2_rn(l[i], p);      // (the sum takes the weights before their rounding)
+        if constexpr (INT8) p = mul2(p, vs[t]);
+        pf[2 * t + i] = pack2<INT8>(p.x, p.y);
       }
     }
     // ---- O += P V
@@ -333,32 +391,30 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
 #pragma unroll
       for (int n = 0; n < NTL; n += 2) {
         uint32_t vf[4];
-        ldsm4t(vf, smem_addr(vp) + R::v_chunk(((lane >> 3) & 1) * 8 + (lane & 7), n + (lane >> 4)) * 16);
+        ldsm4t(vf, vp + R::v_chunk(v_lane, n + (lane >> 4)) * 16);
         mma16<false>(o[n], pf, vf[0], vf[1]);
         mma16<false>(o[n + 1], pf, vf[2], vf[3]);
       }
     } else {
-      // rows 2c, 2c+1, 2c+8, 2c+9, D/8 codes each from channel (D/8) rq: column n of the product's
-      // tile e is channel (D/8) n + e
+      // rows 2c, 2c+1, 2c+8, 2c+9 (one swizzle), D/8 codes each from channel (D/8) rq: column n of the
+      // product's tile e is channel (D/8) n + e
       constexpr int W = D / 32;
       uint32_t v[4][W];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int row = 2 * c + (k & 1) + 8 * (k >> 1);
+        const uint32_t at = kp + v_lane + ((k & 1) + 8 * (k >> 1)) * R::RB;
         if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(vp + R::v_chunk(row, rq) * 16);
-          v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+          const uint4 y = lds16(at);
+          v[k][0] = y.x; v[k][1] = y.y; v[k][2] = y.z; v[k][3] = y.w;
         } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(vp + R::v_chunk(row, rq >> 1) * 16 + 8 * (rq & 1));
-          v[k][0] = x.x; v[k][1] = x.y;
+          const uint2 y = lds8(at);
+          v[k][0] = y.x; v[k][1] = y.y;
         }
-#pragma unroll
-        for (int w = 0; w < W; ++w) v[k][w] ^= 0x80808080u;
       }
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-        const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140), b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+        const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140) ^ 0x80808080u, a1 = __byte_perm(v[0][w], v[1][w], 0x7362) ^ 0x80808080u;
+        const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140) ^ 0x80808080u, b1 = __byte_perm(v[2][w], v[3][w], 0x7362) ^ 0x80808080u;
         mma16<true>(o[4 * w + 0], pf, codes_lo_f16(a0), codes_lo_f16(b0));
         mma16<true>(o[4 * w + 1], pf, codes_hi_f16(a0), codes_hi_f16(b0));
         mma16<true>(o[4 * w + 2], pf, codes_lo_f16(a1), codes_lo_f16(b1));
@@ -371,15 +427,16 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
   // ---- merge the warps: maxima and sums, then the outputs on one scale
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(FULL, l[i], 1);
-    l[i] += __shfl_xor_sync(FULL, l[i], 2);
+    l[i].x += l[i].y;
+    l[i].x += __shfl_xor_sync(FULL, l[i].x, 1);
+    l[i].x += __shfl_xor_sync(FULL, l[i].x, 2);
   }
   __syncthreads();
   float* mo = reinterpret_cast<float*>(smem);
   float2* ml = reinterpret_cast<float2*>(smem + WARPS * 16 * R::PITCH * 4);
   if (c == 0) {
-    ml[warp * 16 + rq] = make_float2(m[0], l[0]);
-    ml[warp * 16 + rq + 8] = make_float2(m[1], l[1]);
+    ml[warp * 16 + rq] = make_float2(m[0], l[0].x);
+    ml[warp * 16 + rq + 8] = make_float2(m[1], l[1].x);
   }
   __syncthreads();
 #pragma unroll
@@ -406,7 +463,7 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
   __syncthreads();
   // eight threads a row
   const int r = tid / 8, e = tid % 8;
-  if (row0 + r >= rows) return;
+  if (r >= rows) return;
   float mx = -INFINITY, sum = 0.0f;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, ml[w * 16 + r].x);
@@ -415,8 +472,8 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
     const float2 x = ml[w * 16 + r];
     sum += x.x == -INFINITY ? 0.0f : x.y * exp2_fast(x.x - mx);
   }
-  const int64_t t = sq.start + (row0 + r) / group;
-  const int h = g * group + (int)((row0 + r) % group);
+  const int64_t t = sq.start + r / group;
+  const int h = g * group + r % group;
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) {
     const int d = 32 * j + 4 * e;
@@ -445,15 +502,16 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
 template <int D>
 __global__ void __launch_bounds__(128)
 attn_join_kernel(const AttnArgs A, const AttnPlan P) {
+  // (launched while the parts are still at work)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const dq_attention& a = A.a;
   const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+  const unsigned row = blockIdx.x * 4 + threadIdx.x / 32;
   const int b = blockIdx.y;
   const SeqBounds sq = seq_bounds(a, b);
-  const int64_t i = row / a.heads;
-  const int h = (int)(row % a.heads);
-  if (i >= sq.n) return;
-  const int splits = sq.len == 0 ? 1 : (int)((sq.len + P.chunk - 1) / P.chunk);
+  const unsigned i = row / (unsigned)a.heads, h = row - i * a.heads;
+  if ((int)i >= sq.n) return;
+  const int chunk = (int)P.chunk, splits = sq.len == 0 ? 1 : (sq.len + chunk - 1) / chunk;
   const int64_t at0 = (sq.start + i) * a.heads + h, pitch = a.tokens * a.heads;
   float mx = -INFINITY;
   for (int s = 0; s < splits; ++s) mx = fmaxf(mx, P.part_ml[s * pitch + at0].x);
@@ -489,11 +547,10 @@ AttnPlan plan_attention(const AttnArgs& A, void* ws) {
   P.row_tiles = (rows + P.tile - 1) / P.tile;
   const int64_t base = std::max<int64_t>(1, P.row_tiles * A.cache.kv_heads * a.sequences);
   if (P.tile == 16) {
-    // enough CTAs for every SM to hold two, none with less than 256 cache rows
-    const int64_t want = (2 * SERVE_SMS + base - 1) / base;
-    const int64_t most = std::max<int64_t>(1, a.max_len / 256);
-    P.splits = std::max<int64_t>(1, std::min(want, most));
-    P.chunk = std::max<int64_t>(64, ((a.max_len + P.splits - 1) / P.splits + 63) / 64 * 64);
+    // about twelve CTAs an SM in all where the sequences are long: lengths differ, and many small
+    // CTAs even out; none with less than 768 cache rows (what a CTA spends besides takes as long as about 200)
+    const int64_t want = (12 * SERVE_SMS + base - 1) / base;
+    P.chunk = std::max<int64_t>(768, ((a.max_len + want - 1) / want + 63) / 64 * 64);
   } else {
     // one CTA per SM: the split with the least (waves) x (tiles of 128 cache rows + what a CTA spends
     // besides, about 2 tiles' time, 4 when its result has to be joined)
@@ -522,9 +579,18 @@ AttnPlan plan_attention(const AttnArgs& A, void* ws) {
 template <int D>
 cudaError_t launch_join(const AttnArgs& A, const AttnPlan& P, cudaStream_t s) {
   const int64_t rows = A.a.max_q * A.a.heads;
-  attn_join_kernel<D><<<dim3((unsigned)((rows + 3) / 4), (unsigned)A.a.sequences), 128, 0, s>>>(A, P);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rows + 3) / 4), (unsigned)A.a.sequences);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, A, P);
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 template <int D, bool INT8>
@@ -533,7 +599,7 @@ cudaError_t launch_kind(const AttnArgs& A, const AttnPlan& P, cudaStream_t s) {
   constexpr auto K = attn_rows_kernel<D, INT8>;
   cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, R::SMEM);
   if (e != cudaSuccess) return e;
-  const int64_t x = P.splits * A.cache.kv_heads * P.row_tiles;
+  const int64_t x = P.splits * A.cache.kv_heads;
   if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
   K<<<dim3((unsigned)x, (unsigned)A.a.sequences), NT, R::SMEM, s>>>(A, P);
   count_launches(1);

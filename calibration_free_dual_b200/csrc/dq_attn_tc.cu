@@ -174,6 +174,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   const int g = (int)(idx / P.splits % G);
   const int64_t rt = P.row_tiles - 1 - idx / P.splits / G;
   const int b = blockIdx.y;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const SeqBounds sq = seq_bounds(a, b);
   if (sq.bad && idx == 0 && tid == 0) atomicOr(A.err_word, ERRBIT_BADARG);
   const int64_t rows = (int64_t)sq.n * group, row0 = rt * 256;
