@@ -18,15 +18,30 @@ namespace {
 constexpr unsigned FULL = 0xFFFFFFFFu;
 constexpr int KV_NT = 256;
 
-// four channels at `p`
+// four channels: as they lie in memory, and as binary32
 template <bool F32IN>
-__device__ __forceinline__ void load4(const char* p, float* x) {
+struct Raw4 {
+  uint32_t u[F32IN ? 4 : 2];
+};
+template <bool F32IN>
+__device__ __forceinline__ Raw4<F32IN> load4(const char* p) {
+  Raw4<F32IN> r;
   if constexpr (F32IN) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    r.u[0] = v.x; r.u[1] = v.y; r.u[2] = v.z; r.u[3] = v.w;
   } else {
     const uint2 v = *reinterpret_cast<const uint2*>(p);      // (q may be rotated in place)
-    const float2 a = bf16x2_to_f2(v.x), b = bf16x2_to_f2(v.y);
+    r.u[0] = v.x; r.u[1] = v.y;
+  }
+  return r;
+}
+template <bool F32IN>
+__device__ __forceinline__ void unpack4(const Raw4<F32IN>& r, float* x) {
+  if constexpr (F32IN) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(r.u[i]);
+  } else {
+    const float2 a = bf16x2_to_f2(r.u[0]), b = bf16x2_to_f2(r.u[1]);
     x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
   }
 }
@@ -52,6 +67,33 @@ kv_append_kernel(const AppendArgs A) {
   const int sub = threadIdx.x % TPR;
   const dq_kv_cache& C = A.cache;
   const int G = C.kv_heads, rows = A.q_heads + 2 * G;
+  // this thread's channels lo..lo+3 and hi..hi+3 of a rotated row
+  const bool halves = A.rot.dim > 0 && !A.rot.interleaved;
+  const bool turned = 8 * sub < A.rot.dim;
+  const int lo_r = halves && turned ? 4 * sub : 8 * sub;
+  const int hi_r = halves && turned ? A.rot.dim / 2 + 4 * sub : 8 * sub + 4;
+  // rows of the token: keys, values, queries. The loads of UNR rounds go ahead of their stores, the
+  // first ones ahead of the token's slot and position too.
+  constexpr int UNR = 4;
+  struct { Raw4<F32IN> lo, hi; } x8[UNR];
+  auto load_rounds = [&](int first) {
+#pragma unroll
+    for (int u = 0; u < UNR; ++u) {
+      const int r = first + u * RPP + threadIdx.x / TPR;
+      const bool is_q = r >= 2 * G, is_v = !is_q && r >= G;
+      const int h = is_q ? r - 2 * G : is_v ? r - G : r;
+      const int lo = is_v ? 8 * sub : lo_r, hi = is_v ? 8 * sub + 4 : hi_r;
+      x8[u] = {};
+      if (r < rows) {
+        const char* src = is_q ? static_cast<const char*>(A.q) + (t * A.q_stride + (int64_t)h * D) * ES
+                          : is_v ? static_cast<const char*>(A.v) + (t * A.v_stride + (int64_t)h * D) * ES
+                                 : static_cast<const char*>(A.k) + (t * A.k_stride + (int64_t)h * D) * ES;
+        x8[u].lo = load4<F32IN>(src + lo * ES);
+        x8[u].hi = load4<F32IN>(src + hi * ES);
+      }
+    }
+  };
+  load_rounds(0);
   const int64_t slot = __ldg(A.slots + t);
   int64_t pos = 0;
   bool ok = slot < C.pages * C.page_size;
@@ -63,32 +105,28 @@ kv_append_kernel(const AppendArgs A) {
     if (threadIdx.x == 0) atomicOr(A.err_word, ERRBIT_BADARG);
     return;
   }
-  // this thread's channels lo..lo+3 and hi..hi+3 of a rotated row
-  const bool halves = A.rot.dim > 0 && !A.rot.interleaved;
-  const bool turned = 8 * sub < A.rot.dim;
-  const int lo_r = halves && turned ? 4 * sub : 8 * sub;
-  const int hi_r = halves && turned ? A.rot.dim / 2 + 4 * sub : 8 * sub + 4;
   float cs[4] = {}, sn[4] = {};
   if (turned) {
-    load4<true>(reinterpret_cast<const char*>(A.rot.cos + pos * (A.rot.dim / 2) + 4 * sub), cs);
-    load4<true>(reinterpret_cast<const char*>(A.rot.sin + pos * (A.rot.dim / 2) + 4 * sub), sn);
+    unpack4<true>(load4<true>(reinterpret_cast<const char*>(A.rot.cos + pos * (A.rot.dim / 2) + 4 * sub)), cs);
+    unpack4<true>(load4<true>(reinterpret_cast<const char*>(A.rot.sin + pos * (A.rot.dim / 2) + 4 * sub)), sn);
   }
-  const int64_t page = slot < 0 ? 0 : slot / C.page_size, prow = slot < 0 ? 0 : slot % C.page_size;
+  const int lg = __ffs(C.page_size) - 1;
+  const int64_t page = slot < 0 ? 0 : slot >> lg, prow = slot < 0 ? 0 : slot & (C.page_size - 1);
   bool bad = false;
-  // rows of the token: keys, values, queries (whole warps run the same count of rounds)
-  for (int r0 = 0; r0 < rows; r0 += RPP) {
-    const int r = r0 + threadIdx.x / TPR;
-    const bool is_q = r >= 2 * G, is_v = !is_q && r >= G;
-    const bool live = r < rows && (is_q || slot >= 0);
-    const int h = is_q ? r - 2 * G : is_v ? r - G : r;
-    const int lo = is_v ? 8 * sub : lo_r, hi = is_v ? 8 * sub + 4 : hi_r;
-    float x[8] = {};
-    if (live) {
-      const char* src = is_q ? static_cast<const char*>(A.q) + (t * A.q_stride + (int64_t)h * D) * ES
-                        : is_v ? static_cast<const char*>(A.v) + (t * A.v_stride + (int64_t)h * D) * ES
-                               : static_cast<const char*>(A.k) + (t * A.k_stride + (int64_t)h * D) * ES;
-      load4<F32IN>(src + lo * ES, x);
-      load4<F32IN>(src + hi * ES, x + 4);
+  // (whole warps run the same count of rounds)
+  for (int first = 0; first < rows; first += UNR * RPP) {
+    if (first > 0) load_rounds(first);
+#pragma unroll
+    for (int u = 0; u < UNR; ++u) {
+      if (first + u * RPP >= rows) break;
+      const int r = first + u * RPP + threadIdx.x / TPR;
+      const bool is_q = r >= 2 * G, is_v = !is_q && r >= G;
+      const bool live = r < rows && (is_q || slot >= 0);
+      const int h = is_q ? r - 2 * G : is_v ? r - G : r;
+      const int lo = is_v ? 8 * sub : lo_r, hi = is_v ? 8 * sub + 4 : hi_r;
+      float x[8];
+      unpack4<F32IN>(x8[u].lo, x);
+      unpack4<F32IN>(x8[u].hi, x + 4);
       if (!is_v && turned) {
         if (halves) {
 #pragma unroll
@@ -98,43 +136,42 @@ kv_append_kernel(const AppendArgs A) {
           for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
         }
       }
-    }
-    const int64_t at = page * C.page_stride + (int64_t)h * C.head_stride + prow * C.row_stride;
-    if (INT8) {
-      uint32_t a = 0;
+      const int64_t at = page * C.page_stride + (int64_t)h * C.head_stride + prow * C.row_stride;
+      if (INT8 && __any_sync(FULL, live && !is_q)) {
+        uint32_t a = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(x[i]) & 0x7FFFFFFFu);
 #pragma unroll
-      for (int off = 1; off < TPR; off <<= 1) a = max(a, __shfl_xor_sync(FULL, a, off));
-      if (live && !is_q) {
-        const bool inf = a >= 0x7F800000u;
-        float d = fmaxf(div_qmax<127>(__uint_as_float(a)), 0x1p-126f), inv = __frcp_rn(d);
-        if (a == 0u) d = inv = 0.0f;
-        if (inf) {
-          d = __uint_as_float(0x7FC00000u);
-          inv = 0.0f;
-          bad = true;
+        for (int off = 1; off < TPR; off <<= 1) a = max(a, __shfl_xor_sync(FULL, a, off));
+        if (live && !is_q) {
+          const bool inf = a >= 0x7F800000u;
+          float d = fmaxf(div_qmax<127>(__uint_as_float(a)), 0x1p-126f), inv = __frcp_rn(d);
+          if (a == 0u) d = inv = 0.0f;
+          if (inf) {
+            d = __uint_as_float(0x7FC00000u);
+            inv = 0.0f;
+            bad = true;
+          }
+          // (rounding as in the row quantizer: no code leaves -127..127)
+          uint32_t b[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            b[i] = __float_as_uint(__fadd_rn(__fmul_rn(x[i], inv), 12582912.0f));
+          uint32_t w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+          uint32_t w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+          if (inf) w0 = w1 = 0u;
+          int8_t* dst = static_cast<int8_t*>(is_v ? C.v : C.k) + at;
+          *reinterpret_cast<uint32_t*>(dst + lo) = w0;
+          *reinterpret_cast<uint32_t*>(dst + hi) = w1;
+          if (sub == 0) (is_v ? C.v_scales : C.k_scales)[(page * G + h) * C.page_size + prow] = d;
         }
-        // (rounding as in the row quantizer: no code leaves -127..127)
-        uint32_t b[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          b[i] = __float_as_uint(__fadd_rn(__fmul_rn(x[i], inv), 12582912.0f));
-        uint32_t w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-        uint32_t w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
-        if (inf) w0 = w1 = 0u;
-        int8_t* dst = static_cast<int8_t*>(is_v ? C.v : C.k) + at;
-        *reinterpret_cast<uint32_t*>(dst + lo) = w0;
-        *reinterpret_cast<uint32_t*>(dst + hi) = w1;
-        if (sub == 0) (is_v ? C.v_scales : C.k_scales)[(page * G + h) * C.page_size + prow] = d;
-        continue;
       }
-    }
-    if (live) {
-      char* dst = is_q ? static_cast<char*>(A.q_out) + (t * A.q_out_stride + (int64_t)h * D) * 2
-                       : static_cast<char*>(is_v ? C.v : C.k) + at * 2;
-      *reinterpret_cast<uint2*>(dst + lo * 2) = pack4(x);
-      *reinterpret_cast<uint2*>(dst + hi * 2) = pack4(x + 4);
+      if (live && (!INT8 || is_q)) {
+        char* dst = is_q ? static_cast<char*>(A.q_out) + (t * A.q_out_stride + (int64_t)h * D) * 2
+                         : static_cast<char*>(is_v ? C.v : C.k) + at * 2;
+        *reinterpret_cast<uint2*>(dst + lo * 2) = pack4(x);
+        *reinterpret_cast<uint2*>(dst + hi * 2) = pack4(x + 4);
+      }
     }
   }
   if (bad) atomicOr(A.err_word, ERRBIT_NONFINITE);

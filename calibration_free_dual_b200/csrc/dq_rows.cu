@@ -115,49 +115,70 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[CH], const RowScale& s)
   return w;
 }
 
-template <bool F32IN, int V>
+// RD rows of a CTA in flight
+template <bool F32IN, int V, int RD>
 __global__ void __launch_bounds__(MAX_NT)
 row_quant_kernel(const RowsArgs A) {
   // a product launched behind this kernel may start loading its weight
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int Q = F32IN ? 2 : 1;                  // 16-byte pieces of a chunk
+  extern __shared__ __align__(16) uint4 ring[];      // [RD][V][Q][threads]
   __shared__ uint32_t slots[2][MAX_NT / 32];
   const int64_t chunks = A.n / CH, step = A.ldx * (F32IN ? 4 : 2);
-  const char* X = static_cast<const char*>(A.X);
+  const int nt = blockDim.x, tid = threadIdx.x;
+  const char* X = static_cast<const char*>(A.X) + (int64_t)tid * CH * (F32IN ? 4 : 2);
+  const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring + tid));
   float c[V][CH];
   bool in[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int64_t k = threadIdx.x + (int64_t)i * blockDim.x;
-    in[i] = k < chunks;
-    load_c8(A.c, k, in[i], c[i]);
+    in[i] = tid + (int64_t)i * nt < chunks;
+    load_c8(A.c, tid + (int64_t)i * nt, in[i], c[i]);
   }
-  Raw8<F32IN> next[V] = {};
-  auto fetch = [&](int64_t row) {
+  auto fetch = [&](int64_t row, int slot) {
+    if (row < A.rows) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (in[i]) next[i] = load8<F32IN>(X + row * step, threadIdx.x + (int64_t)i * blockDim.x);
+      for (int i = 0; i < V; ++i)
+        if (in[i]) {
+          const char* src = X + row * step + (int64_t)i * nt * CH * (F32IN ? 4 : 2);
+#pragma unroll
+          for (int h = 0; h < Q; ++h)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                         :: "r"(mine + (uint32_t)(((slot * V + i) * Q + h) * nt) * 16u), "l"(src + 16 * h) : "memory");
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  fetch(blockIdx.x);                                // the grid has at most `rows` CTAs
-  int parity = 0;
+  const int64_t stride = gridDim.x;
+#pragma unroll
+  for (int d = 0; d < RD; ++d) fetch(blockIdx.x + d * stride, d);
+  int parity = 0, slot = 0;
   bool bad = false;
-  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, parity ^= 1) {
+  for (int64_t row = blockIdx.x; row < A.rows; row += stride, parity ^= 1) {
+    asm volatile("cp.async.wait_group %0;" :: "n"(RD - 1) : "memory");
     float x[V][CH];
     uint32_t a = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      rescale8<F32IN>(next[i], c[i], x[i]);
+      Raw8<F32IN> r = {};
+      if (in[i]) {
+#pragma unroll
+        for (int h = 0; h < Q; ++h) r.u[h] = ring[((slot * V + i) * Q + h) * nt + tid];
+      }
+      rescale8<F32IN>(r, c[i], x[i]);
       a = max(a, absmax_bits(x[i]));
     }
-    if (row + gridDim.x < A.rows) fetch(row + gridDim.x);
+    fetch(row + RD * stride, slot);                  // this thread's chunks are in registers
+    slot = slot + 1 == RD ? 0 : slot + 1;
     const RowScale s = row_scale(block_max(a, slots, parity));
     bad |= s.bad;
-    if (threadIdx.x == 0) A.scales[row] = s.d;
+    if (tid == 0) A.scales[row] = s.d;
     uint2* dst = reinterpret_cast<uint2*>(A.codes + row * A.n);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (in[i]) dst[threadIdx.x + (int64_t)i * blockDim.x] = codes8(x[i], s);
+      if (in[i]) dst[tid + (int64_t)i * nt] = codes8(x[i], s);
   }
-  if (bad && threadIdx.x == 0) atomicOr(A.err_word, ERRBIT_NONFINITE);
+  if (bad && tid == 0) atomicOr(A.err_word, ERRBIT_NONFINITE);
 }
 
 // rows longer than the registers of one CTA: one pass for the maximum, one for the codes
@@ -191,21 +212,36 @@ row_quant_long_kernel(const RowsArgs A) {
   if (bad && threadIdx.x == 0) atomicOr(A.err_word, ERRBIT_NONFINITE);
 }
 
+template <bool F32IN, int V>
+cudaError_t launch_v(const RowsArgs& A, int nt, cudaStream_t s) {
+  constexpr int RD = F32IN && V == 4 ? 2 : 4;
+  constexpr auto K = row_quant_kernel<F32IN, V, RD>;
+  const int smem = RD * V * nt * CH * (F32IN ? 4 : 2);
+  const cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  // as many CTAs as the SMs hold at a time (threads; registers for the wider ones; shared memory)
+  const int64_t hold = std::max(1, std::min(2048 / nt / (V == 4 ? 2 : 1), 224 * 1024 / (smem + 1280)));
+  K<<<(unsigned)std::min<int64_t>(A.rows, SERVE_SMS * hold), nt, smem, s>>>(A);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
 template <bool F32IN>
 cudaError_t launch_rows(const RowsArgs& A, cudaStream_t s) {
   const int64_t chunks = A.n / CH;
-  // the fewest chunks a thread that fit a CTA: short rows get many threads, hence low latency
-  const int v = chunks <= MAX_NT ? 1 : chunks <= 2 * MAX_NT ? 2 : chunks <= 4 * MAX_NT ? 4 : 0;
+  // few rows: the fewest chunks a thread that fit a CTA, for latency. Rows enough for all SMs: four chunks a
+  // thread, so that more and smaller CTAs overlap their barriers (8192 x 4096 bf16: 26.6 us with one
+  // chunk a thread, 512 threads).
+  int v = chunks <= MAX_NT ? 1 : chunks <= 2 * MAX_NT ? 2 : chunks <= 4 * MAX_NT ? 4 : 0;
+  if (v != 0 && A.rows > 4 * SERVE_SMS) v = chunks >= 4 * 64 ? 4 : chunks >= 2 * 64 ? 2 : 1;
   const int nt = v == 0 ? MAX_NT : (int)align_up((size_t)(chunks + v - 1) / v, 32);
-  // as many CTAs as the SMs hold at a time (2048 threads each)
-  const int64_t ctas = std::min<int64_t>(A.rows, (int64_t)SERVE_SMS * std::max(1, 2048 / nt / (v == 4 ? 2 : 1)));
-  const unsigned g = (unsigned)ctas;
   switch (v) {
-    case 1: row_quant_kernel<F32IN, 1><<<g, nt, 0, s>>>(A); break;
-    case 2: row_quant_kernel<F32IN, 2><<<g, nt, 0, s>>>(A); break;
-    case 4: row_quant_kernel<F32IN, 4><<<g, nt, 0, s>>>(A); break;
-    default: row_quant_long_kernel<F32IN><<<g, nt, 0, s>>>(A); break;
+    case 1: return launch_v<F32IN, 1>(A, nt, s);
+    case 2: return launch_v<F32IN, 2>(A, nt, s);
+    case 4: return launch_v<F32IN, 4>(A, nt, s);
+    default: break;
   }
+  row_quant_long_kernel<F32IN><<<(unsigned)std::min<int64_t>(A.rows, 4 * SERVE_SMS), nt, 0, s>>>(A);
   count_launches(1);
   return cudaGetLastError();
 }
