@@ -103,6 +103,15 @@ __device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t* 
          "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+         "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+         "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -122,7 +131,8 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 __device__ __forceinline__ float f_of(uint32_t u) { return __uint_as_float(u); }
 
-constexpr int POLY = 2;                           // of 8 groups of four weights, those with a pair by polynomial
+constexpr int P_HEAD = 96;                         // weights of a tile whose product does not wait for the rest's exponentials
+constexpr int POLY = 3;                            // of 8 groups of four weights, those with a pair by polynomial
 constexpr float C0 = 0.9999992847442627f, C1 = 0.6931217908859253f, C2 = 0.240247443318367f,
                 C3 = 0.05591785907745361f, C4 = 0.009570102207362652f;
 // 2^y of a pair by the FMA pipe: y = n + f with n the nearest integer (added and removed 1.5 2^23), 2^f on
@@ -143,6 +153,8 @@ __device__ __forceinline__ float2 exp2_poly(float2 y) {
   return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
+
+template <int N> struct Int { static constexpr int value = N; };
 
 template <int N> __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
@@ -197,7 +209,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   unsigned char* base = smem_raw + (sbase - raw);
   const uint32_t full0 = sbase + T::BAR_OFF, empty0 = full0 + 8 * SLOTS;
   const uint32_t sfull0 = empty0 + 8 * SLOTS, pready0 = sfull0 + 16, ofull0 = pready0 + 16;
-  const uint32_t phalf0 = ofull0 + 16, qready = phalf0 + 16, vtail = qready + 8;
+  const uint32_t phead0 = ofull0 + 16, qready = phead0 + 16, vtail = qready + 8;
   const uint32_t rawfull0 = vtail + 8, rawempty0 = rawfull0 + 8 * T::RAW_SLOTS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + T::BAR_OFF + 8 * (2 * SLOTS + 10 + 2 * T::RAW_SLOTS));
   volatile int* fail = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -211,7 +223,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     for (int t = 0; t < 2; ++t) {
       mbar_init(sfull0 + 8 * t, 1);
       mbar_init(pready0 + 8 * t, 4);
-      mbar_init(phalf0 + 8 * t, 4);
+      mbar_init(phead0 + 8 * t, 4);
       mbar_init(ofull0 + 8 * t, 1);
     }
     for (int s = 0; s < T::RAW_SLOTS; ++s) {
@@ -287,7 +299,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     float l = 0.0f, vlog = V_LOW;                   // INT8: log2 of the values' unit
     bool ok = true;
     for (int j = 0; j < nt[t]; ++j) {
-      if (!mbar_wait(sfull0 + 8 * t, (uint32_t)j & 1u) || *fail) { ok = false; break; }
+      if (!mbar_wait(sfull0 + 8 * t, (uint32_t)j & 1u)) { ok = false; break; }
       tc_fence_after();
       if (warp_there) {
         const int left = lim - j * KT;               // columns from here on are masked
@@ -355,17 +367,17 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         // ---- weights, over the scores' columns (all of which have been read)
         float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
         const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+        auto weights = [&](auto from, auto to) {
+          constexpr int FROM = decltype(from)::value, TO = decltype(to)::value;
+          uint32_t p[(TO - FROM) / 2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t p[32];
-#pragma unroll
-          for (int i = 0; i < 64; i += 4) {
-            const uint32_t* x = s + 64 * q + i;
-            float2 y0 = fma2(make_float2(f_of(x[0]), f_of(x[1])), c2, r2);
-            float2 y1 = fma2(make_float2(f_of(x[2]), f_of(x[3])), c2, r2);
-            // the exponential unit gives 16 results a clock to the SM, as long for a tile as its
-            // products take: part of the pairs goes to the FMA pipe
-            if ((i / 2) % 16 < 2 * POLY) {
+          for (int i = FROM; i < TO; i += 4) {
+            float2 y0 = fma2(make_float2(f_of(s[i]), f_of(s[i + 1])), c2, r2);
+            float2 y1 = fma2(make_float2(f_of(s[i + 2]), f_of(s[i + 3])), c2, r2);
+            // The exponential unit gives 16 results a clock to the SM: as long for a tile as its
+            // products take. bf16: part of the pairs goes to the FMA pipe (1000 tokens over 24000 rows,
+            // 64 channels: 332 -> 316 us); INT8 has no registers to spare for it.
+            if (!INT8 && (i / 4) % 8 < POLY) {
               y0 = exp2_poly(y0);
             } else {
               y0.x = exp2_fast(y0.x); y0.y = exp2_fast(y0.y);
@@ -374,26 +386,27 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             l0 = __fadd2_rn(l0, y0);
             l1 = __fadd2_rn(l1, y1);
             if constexpr (INT8) {
-              const float4 v4 = *reinterpret_cast<const float4*>(vs + 64 * q + i);
+              const float4 v4 = *reinterpret_cast<const float4*>(vs + i);
               y0 = mul2(y0, make_float2(v4.x, v4.y));
               y1 = mul2(y1, make_float2(v4.z, v4.w));
             }
-            p[i / 2] = pack16<INT8>(y0.x, y0.y);
-            p[i / 2 + 1] = pack16<INT8>(y1.x, y1.y);
+            p[(i - FROM) / 2] = pack16<INT8>(y0.x, y0.y);
+            p[(i - FROM) / 2 + 1] = pack16<INT8>(y1.x, y1.y);
           }
-          tmem_st32_async(s_addr + 32 * q, p);
-          if (q == 0) {
-            // the first half of the weights' product starts under the second half's exponentials
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(phalf0 + 8 * t);
-          }
-        }
+#pragma unroll
+          for (int w = 0; w < (TO - FROM) / 2; w += 16) tmem_st16_async(s_addr + FROM / 2 + w, p + w);
+        };
+        weights(Int<0>{}, Int<P_HEAD>{});
+        // the product of the first weights starts under the last ones' exponentials
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(phead0 + 8 * t);
+        weights(Int<P_HEAD>{}, Int<KT>{});
         l += (l0.x + l0.y) + (l1.x + l1.y);
         tmem_wait_st();
       } else if (lane == 0) {
-        mbar_arrive(phalf0 + 8 * t);
+        mbar_arrive(phead0 + 8 * t);
       }
       tc_fence_before();
       __syncwarp();
@@ -456,56 +469,52 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                  operand_desc(k + (s >> 2) * T::HALF + 32 * (s & 3)), ID_S, s > 0, elected);
         mma_commit_if(elected, sfull0 + 8 * t);
       };
-      auto outputs = [&](int t, int slot, bool first, int half) {
+      auto outputs = [&](int t, int slot, bool first, int from, int to) {
         const uint32_t v = sbase + T::KV_OFF + slot * T::TILE;
 #pragma unroll
-        for (int s = half * KT / 32; s < (half + 1) * KT / 32; ++s)
+        for (int s = from; s < to; ++s)
           mma_ts(utm + T::O_COL + D * t, utm + 128 * t + 8 * s, v_desc(v + 2048 * s), ID_O, !first || s > 0, elected);
       };
-      bool ok = mbar_wait_warp(qready, 0) && mbar_wait_warp(full0, 0) && !warp_any(*fail);
-      if (ok) {
+      bool bad = false;                              // a wait has given up (looked at once a tile)
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!bad && !mbar_try(bar, parity)) bad = !mbar_wait(bar, parity);
+        __syncwarp();
         tc_fence_after();
+      };
+      wait(qready, 0);
+      wait(full0, 0);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (unt[t] > 0) scores(t, 0);
-        mma_commit_if(elected, empty0);
-      }
-      for (int j = 0; j < un && ok; ++j) {
+      for (int t = 0; t < 2; ++t)
+        if (unt[t] > 0) scores(t, 0);
+      mma_commit_if(elected, empty0);
+      for (int j = 0; j < un && !warp_any(bad); ++j) {
         const int vi = 2 * j + 1, ki = 2 * j + 2;
         const int vslot = vi % SLOTS, kslot = ki % SLOTS;
         bool v_here = false, k_here = false;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (!ok) break;
           if (j < unt[t]) {
-            ok = mbar_wait_warp(phalf0 + 8 * t, (uint32_t)j & 1u) && !warp_any(*fail);
-            if (ok && !v_here) {
-              ok = mbar_wait_warp(full0 + 8 * vslot, (uint32_t)(vi / SLOTS) & 1u) && !warp_any(*fail);
-              if (ok && utail && j == un - 1) ok = mbar_wait_warp(vtail, 0) && !warp_any(*fail);
+            if (!v_here) {
+              wait(full0 + 8 * vslot, (uint32_t)(vi / SLOTS) & 1u);
+              if (utail && j == un - 1) wait(vtail, 0);
               v_here = true;
             }
-            if (!ok) break;
-            tc_fence_after();
-            outputs(t, vslot, j == 0, 0);
-            ok = mbar_wait_warp(pready0 + 8 * t, (uint32_t)j & 1u) && !warp_any(*fail);
-            if (!ok) break;
-            tc_fence_after();
-            outputs(t, vslot, j == 0, 1);
+            wait(phead0 + 8 * t, (uint32_t)j & 1u);
+            outputs(t, vslot, j == 0, 0, P_HEAD / 16);
+            wait(pready0 + 8 * t, (uint32_t)j & 1u);
+            outputs(t, vslot, false, P_HEAD / 16, KT / 16);
             if (j == unt[t] - 1) mma_commit_if(elected, ofull0 + 8 * t);
           }
           if (j + 1 < unt[t]) {
-            if (!k_here) ok = mbar_wait_warp(full0 + 8 * kslot, (uint32_t)(ki / SLOTS) & 1u) && !warp_any(*fail);
+            if (!k_here) wait(full0 + 8 * kslot, (uint32_t)(ki / SLOTS) & 1u);
             k_here = true;
-            if (!ok) break;
-            tc_fence_after();
             scores(t, kslot);
           }
         }
-        if (!ok) break;
         mma_commit_if(elected, empty0 + 8 * vslot);
         if (j + 1 < un) mma_commit_if(elected, empty0 + 8 * kslot);
       }
-      if (!ok) *fail = 1;
+      if (bad) *fail = 1;
     }
     } else if (warp == 9) {
     // ================================================================= pages by TMA
@@ -534,7 +543,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       for (int kv = 0; kv < 2; ++kv) {
         const int slot = i % RING;
         const uint32_t bar = rfull + 8 * slot;
-        if (!mbar_wait_warp(rempty + 8 * slot, ((uint32_t)(i / RING) & 1u) ^ 1u) || warp_any(*fail)) {
+        if (!mbar_wait_warp(rempty + 8 * slot, ((uint32_t)(i / RING) & 1u) ^ 1u)) {
           ok = false;
           break;
         }
@@ -597,8 +606,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     fetch_scales(0);
     for (int i = 0; i < 2 * n && ok; ++i) {
       const int slot = i % SLOTS, rslot = i % T::RAW_SLOTS, j = i >> 1;
-      ok = mbar_wait(rawfull0 + 8 * rslot, (uint32_t)(i / T::RAW_SLOTS) & 1u) && !*fail;
-      ok = ok && mbar_wait(empty0 + 8 * slot, ((uint32_t)(i / SLOTS) & 1u) ^ 1u) && !*fail;
+      ok = mbar_wait(rawfull0 + 8 * rslot, (uint32_t)(i / T::RAW_SLOTS) & 1u);
+      ok = ok && mbar_wait(empty0 + 8 * slot, ((uint32_t)(i / SLOTS) & 1u) ^ 1u);
       if (!ok) break;
       const int valid = sq.len - (int)kb - j * KT;   // rows past them may be anything: zeros
       const uint4* src = reinterpret_cast<const uint4*>(base + T::RAW_OFF + rslot * T::RAW);

@@ -54,20 +54,6 @@ __device__ __forceinline__ void mma_i8(uint32_t tmem_d, uint64_t adesc, uint64_t
         :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected) : "memory");
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// a shared-memory address of this CTA, as the same place in CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
 __device__ __forceinline__ int4 ld_cluster4(uint32_t addr) {
   int4 v;
   asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
@@ -259,17 +245,6 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       " [%0], [%1, {%2, %3}], [%4];"
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
 }
-// completes when all products issued so far have, on the barrier of that place in both CTAs
-__device__ __forceinline__ void commit_pair(uint32_t elected, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}"
-      :: "r"(bar), "r"(elected), "h"((uint16_t)3) : "memory");
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-
 // tile index -> weight and token tile: 8 token tiles wide, so that the tiles in flight share operands
 __device__ __forceinline__ void tile_at(int64_t idx, const Plan8& P, int64_t& nt, int64_t& tt) {
   constexpr int64_t WIDE = 8;
@@ -297,8 +272,7 @@ gemm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
   const uint32_t lead_full0 = map_rank(full0, 0), lead_accempty0 = map_rank(accempty0, 0);
 
   if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(&tmem_slot)), "r"(512u) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    tmem_alloc_pair(smem_u32(&tmem_slot), 512);
   }
   if (tid == 32) {
     for (int s = 0; s < PAIR_STAGES; ++s) {
@@ -421,7 +395,7 @@ gemm8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
   if (warp == 0) {
     __syncwarp();
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512u) : "memory");
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 

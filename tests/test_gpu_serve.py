@@ -390,7 +390,7 @@ def test_attention(dq, kind, H, G, D, news, lens):
 @pytest.mark.parametrize("kind", [torch.bfloat16, torch.int8])
 @pytest.mark.parametrize("S", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("layout", ["head", "token", "pair"])
-@pytest.mark.parametrize("n", [1, 90])
+@pytest.mark.parametrize("n", [1, 90, 300])
 def test_attention_page_sizes_and_layouts(dq, kind, S, layout, n):
     rng = np.random.default_rng(S + n)
     news, lens = [n, n], [n + 301, n]
