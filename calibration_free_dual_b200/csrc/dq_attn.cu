@@ -366,8 +366,9 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
       vunit = unit;
       vinv = 0x1p15f / unit;
     }
-    // ---- P
-    uint32_t pf[4];
+    // ---- P. bf16 has 8 bits, so a weight goes as two of them (its rounding, and what that leaves): the
+    // tensor cores have time to spare, and the result's error is then its own last rounding
+    uint32_t pf[4], pr[4];
     if constexpr (INT8) {
       const float2 v2 = make_float2(vinv, vinv);
       vs[0] = mul2(vs[0], v2);
@@ -384,6 +385,10 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
         l[i] = __fadd2_rn(l[i], p);      // (the sum takes the weights before their rounding)
         if constexpr (INT8) p = mul2(p, vs[t]);
         pf[2 * t + i] = pack2<INT8>(p.x, p.y);
+        if constexpr (!INT8) {
+          const float2 hi = bf16x2_to_f2(pf[2 * t + i]);
+          pr[2 * t + i] = pack2<false>(p.x - hi.x, p.y - hi.y);
+        }
       }
     }
     // ---- O += P V
@@ -394,6 +399,8 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
         ldsm4t(vf, vp + R::v_chunk(v_lane, n + (lane >> 4)) * 16);
         mma16<false>(o[n], pf, vf[0], vf[1]);
         mma16<false>(o[n + 1], pf, vf[2], vf[3]);
+        mma16<false>(o[n], pr, vf[0], vf[1]);
+        mma16<false>(o[n + 1], pr, vf[2], vf[3]);
       }
     } else {
       // rows 2c, 2c+1, 2c+8, 2c+9 (one swizzle), D/8 codes each from channel (D/8) rq: column n of the

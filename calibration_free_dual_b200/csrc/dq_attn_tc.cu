@@ -292,7 +292,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const bool warp_there = row0 + 128 * t + sp * 32 < rows;
     float c = fabsf(a.scale) * 1.4426950408889634f;
     if (INT8) c /= qfac[128 * t + r];
-    c = fmaxf(c, 1e-37f);                          // (a masked score stays -inf)
+    c = fmaxf(c, 0x1p-126f);                        // (a masked score stays -inf)
     const uint32_t s_addr = tmem + ((uint32_t)(sp * 32) << 16) + 128 * t;
     const uint32_t o_addr = tmem + ((uint32_t)(sp * 32) << 16) + T::O_COL + D * t;
     float ref = -INFINITY;                          // exponent's reference: weights are exp2(c s - ref)

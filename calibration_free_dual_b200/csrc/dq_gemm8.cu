@@ -79,6 +79,12 @@ struct Plan8 {
 
 constexpr int SPLIT_STAGES_MAX = 8;
 constexpr int PARTS_MAX = 8;             // CTAs of a cluster
+// A CTA of a cluster waits for the others, and the allocation of tensor memory waits for whoever holds
+// it. Clusters of different streams could so wait for one another in a circle, were their CTAs on the
+// same SMs. Shared memory keeps them apart: a CTA of a pair leaves less than this, and the split CTAs
+// that fit an SM together need no more than its 512 columns (40 KB a CTA hold at most 64 columns, 49
+// KB 128, 97 KB 256).
+constexpr int SPLIT_SMEM_MIN = 39 * 1024;
 
 template <bool BF16OUT>
 __global__ void __launch_bounds__(GT)
@@ -237,6 +243,7 @@ gemm8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
 constexpr int PAIR_STAGES = 6;
 constexpr int PAIR_STAGE = 2 * BM * BK;             // 128 weight rows, up to 128 token rows
 constexpr int PAIR_SMEM = PAIR_STAGES * PAIR_STAGE + 1024;
+static_assert(PAIR_SMEM + SPLIT_SMEM_MIN > 227 * 1024 && 2 * PAIR_SMEM > 227 * 1024, "never on one SM");
 
 // a TMA tile load that completes on an mbarrier of the pair's first CTA
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -464,7 +471,7 @@ Plan8 plan_gemm8(int64_t T, int64_t N, int64_t K) {
     const int budget = (best.bn <= 64 ? 108 : 216) * 1024;      // narrow tiles: two CTAs an SM
     best.stages = std::min<int>({SPLIT_STAGES_MAX, budget / stage, best.per});
     const int red = best.parts > 1 ? best.bn * BM * 4 : 0;
-    best.smem = std::max(best.stages * stage, red) + 1024;
+    best.smem = std::max({best.stages * stage, red, SPLIT_SMEM_MIN}) + 1024;
   }
   return best;
 }

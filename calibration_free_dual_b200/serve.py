@@ -43,10 +43,11 @@ def _expect(t, dev: int, name: str, dtype) -> None:
 
 def _vector(t, dev: int, name: str, n: int, dtype) -> int:
     """Address of a contiguous vector of n entries."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype
+            and t.shape == (n,) and t.is_contiguous()):
+        return t.data_ptr()
     _expect(t, dev, name, dtype)
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError("%s must be contiguous with %d entries" % (name, n))
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous with %d entries" % (name, n))
 
 
 def _scratch(workspace, need: int, like: torch.Tensor) -> torch.Tensor:
@@ -201,7 +202,8 @@ def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, dtype=tor
 
 def _cache_of(cache: dict, dev: int) -> _lib.dq_kv_cache:
     k, v = cache["k"], cache["v"]
-    dtype = getattr(k, "dtype", None)
+    _need_cuda(k, "cache k")
+    dtype = k.dtype
     if dtype not in CACHE_TYPES:
         raise TypeError("the cache must be bfloat16 or int8, got %s" % dtype)
     _expect(k, dev, "cache k", dtype)
@@ -222,23 +224,24 @@ def _cache_of(cache: dict, dev: int) -> _lib.dq_kv_cache:
                                 hs, rs, None, None)
     ks, vs = cache["k_scales"], cache["v_scales"]
     for t, name in ((ks, "cache k_scales"), (vs, "cache v_scales")):
-        _expect(t, dev, name, torch.float32)
-        if t.shape != shape[:3] or not t.is_contiguous():
+        if (not isinstance(t, torch.Tensor) or t.dtype is not torch.float32
+                or t.get_device() != dev or t.shape != shape[:3] or not t.is_contiguous()):
+            _expect(t, dev, name, torch.float32)
             raise ValueError(name + " must be contiguous [pages, kv_heads, page_size]")
     return _lib.dq_kv_cache(_lib.DQ_CACHE_INT8, S, D, G, P, k.data_ptr(), v.data_ptr(), ps, hs,
                             rs, ks.data_ptr(), vs.data_ptr())
 
 
-def _heads(x: torch.Tensor, name: str, T: int, D: int):
-    """(heads, token stride) of [T, heads, D] with contiguous heads."""
-    shape = x.shape
-    if len(shape) != 3 or shape[0] != T or shape[2] != D:
-        raise ValueError("%s must be [%d, heads, %d]" % (name, T, D))
-    H = shape[1]
-    t, h, d = x.stride()
-    if T > 0 and (d != 1 or (H > 1 and h != D)):
+def _heads(x: torch.Tensor, dev: int, name: str, dtype, T: int, H: int, D: int) -> int:
+    """Token stride of [T, H, D] of the call's device and dtype with contiguous heads."""
+    if (isinstance(x, torch.Tensor) and x.get_device() == dev and x.dtype is dtype
+            and x.shape == (T, H, D)):
+        t, h, d = x.stride()
+        if (d == 1 and (h == D or H == 1)) or T == 0:
+            return t if T > 1 else H * D
         raise ValueError("%s must have contiguous heads and channels" % name)
-    return H, (t if T > 1 else H * D)
+    _expect(x, dev, name, dtype)
+    raise ValueError("%s must be [%d, %d, %d]" % (name, T, H, D))
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: dict, slots: torch.Tensor,
@@ -254,14 +257,12 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: dict, slots: torch.Tensor
     if stream is not None or dev != _device():
         with _place(k, stream):
             return kv_append(k, v, cache, slots, positions, cos, sin, q, interleaved, q_out)
+    dtype = k.dtype
     dt = _dtype_code(k)
-    _expect(v, dev, "v", k.dtype)
     c = _cache_of(cache, dev)
     T, D, G = k.shape[0] if k.dim() else 0, c.head_dim, c.kv_heads
-    kh, ks = _heads(k, "k", T, D)
-    vh, vs = _heads(v, "v", T, D)
-    if kh != G or vh != G:
-        raise ValueError("k and v must have the cache's %d heads" % G)
+    ks = _heads(k, dev, "k", dtype, T, G, D)
+    vs = _heads(v, dev, "v", dtype, T, G, D)
     sp = _vector(slots, dev, "slots", T, torch.int64)
     rot = None
     if positions is not None or cos is not None or sin is not None:
@@ -270,25 +271,23 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: dict, slots: torch.Tensor
         pp = _vector(positions, dev, "positions", T, torch.int32)
         _expect(cos, dev, "cos", torch.float32)
         _expect(sin, dev, "sin", torch.float32)
-        if cos.dim() != 2 or sin.shape != cos.shape or not (cos.is_contiguous()
-                                                            and sin.is_contiguous()):
+        shape = cos.shape
+        if len(shape) != 2 or sin.shape != shape or not (cos.is_contiguous()
+                                                         and sin.is_contiguous()):
             raise ValueError("cos and sin must be contiguous [rows, dim / 2]")
-        rows, half = cos.shape
+        rows, half = shape
         rot = ctypes.byref(_lib.dq_rotary(cos.data_ptr(), sin.data_ptr(), pp, rows, 2 * half,
                                           1 if interleaved else 0))
     qp = op = None
     H = qs = os = 0
     if q is not None:
-        _expect(q, dev, "q", k.dtype)
-        H, qs = _heads(q, "q", T, D)
+        H = q.shape[1] if q.dim() == 3 else 0
+        qs = _heads(q, dev, "q", dtype, T, H, D)
         if q_out is None:
             os = H * D
             q_out = _alloc((T, H, D), (os, D, 1), dtype=torch.bfloat16, device=k.device)
         else:
-            _expect(q_out, dev, "q_out", torch.bfloat16)
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must have q's shape")
-            os = _heads(q_out, "q_out", T, D)[1]
+            os = _heads(q_out, dev, "q_out", torch.bfloat16, T, H, D)
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -316,11 +315,9 @@ def paged_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor,
         with _place(q, stream):
             return paged_attention(q, cache, page_table, lengths, q_starts, max_q, max_len,
                                    causal, scale, out, None, workspace)
-    if q.dtype is not torch.bfloat16:
-        raise TypeError("q must be bfloat16, got %s" % q.dtype)
     c = _cache_of(cache, dev)
-    T, D = q.shape[0] if q.dim() else 0, c.head_dim
-    H, qs = _heads(q, "q", T, D)
+    T, H, D = (*q.shape[:2], c.head_dim) if q.dim() == 3 else (0, 0, c.head_dim)
+    qs = _heads(q, dev, "q", torch.bfloat16, T, H, D)
     _expect(page_table, dev, "page_table", torch.int32)
     if page_table.dim() != 2:
         raise ValueError("page_table must be 2-D row-major")
@@ -348,10 +345,7 @@ def paged_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor,
         os = H * D
         out = _alloc((T, H, D), (os, D, 1), dtype=torch.bfloat16, device=q.device)
     else:
-        _expect(out, dev, "out", torch.bfloat16)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        os = _heads(out, "out", T, D)[1]
+        os = _heads(out, dev, "out", torch.bfloat16, T, H, D)
     a = _lib.dq_attention(q.data_ptr(), out.data_ptr(), qs, os, T, B, H, 1 if causal else 0, sp,
                           lp, page_table.data_ptr(), pitch, max_q, max_len,
                           D ** -0.5 if scale is None else scale)

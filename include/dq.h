@@ -373,8 +373,9 @@ DQ_API dq_status dq_kv_append(const dq_kv_cache* cache, int64_t tokens, int32_t 
  *               them is not computed, and raises DQ_ERR_INVALID_ARG in the device error word
  * heads is a multiple of kv_heads, at most 128 times as many. Cache rows past a sequence's length may hold anything. A page
  * number outside [0, pages) raises DQ_ERR_INVALID_ARG in the device error word (its rows count
- * as zeros). Scores and softmax statistics are binary32; the weights of a tile are rounded to
- * bf16 (bf16 cache) or fp16 (INT8 cache) for the product with v. */
+ * as zeros). Scores and softmax statistics are binary32. For the product with v the weights of
+ * a tile are rounded: to fp16 (INT8 cache), to bf16 (bf16 cache; with at most 16 rows of tokens and heads a key
+ * head, to two bf16). INT8 value scales are followed from 2^-80 to 2^90. */
 typedef struct {
   const void* q;
   void* out;

@@ -622,3 +622,142 @@ def test_two_calls_share_one_workspace_in_stream_order(dq):
     a = dq.paged_attention(q, cache, table, lt, workspace=ws)
     b = dq.paged_attention(q.flip(0).contiguous(), cache, table.flip(0).contiguous(), lt.flip(0).contiguous(), workspace=ws)
     assert torch.equal(a, b.flip(0))
+
+
+# ------------------------------------------------------------------- calls around the edges
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.int8])
+@pytest.mark.parametrize("n", [1, 60, 300])
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-6])
+def test_attention_odd_scales(dq, kind, n, scale):
+    rng = np.random.default_rng(n)
+    news, lens = [n], [n + 100]
+    q, cache, table, lt, st, tn = _setup(rng, dq, news, lens, 4, 2, 128, 32, kind)
+    _poison(cache, tn, lens, 32)
+    o = dq.paged_attention(q, cache, table, lt, q_starts=st, scale=scale)
+    _check_attention(o, q, cache, tn, lens, news, True, scale)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.int8])
+@pytest.mark.parametrize("n", [1, 70])
+def test_split_attention_in_a_graph(dq, kind, n):
+    """Sequences split over CTAs and joined, captured and replayed over new queries, new lengths and
+    a new table in the same tensors."""
+    rng = np.random.default_rng(n)
+    news, lens = [n, n], [6000, 4001]
+    q, cache, table, lt, st, tn = _setup(rng, dq, news, lens, 8, 2, 128, 64, kind)
+    kw = dict(q_starts=st, max_q=n, max_len=6000)
+    dq.paged_attention(q, cache, table, lt, **kw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = dq.paged_attention(q, cache, table, lt, **kw)
+    for lens in ([6000, 4001], [n, 5999]):
+        table.copy_(torch.from_numpy(tn).cuda() % cache["k"].shape[0])
+        lt.copy_(torch.tensor(lens, dtype=torch.int32))
+        q.copy_(torch.from_numpy(rng.standard_normal(q.shape).astype(np.float32)).to(torch.bfloat16))
+        graph.replay()
+        _check_attention(o, q, cache, table.cpu().numpy(), lens, news, True)
+
+
+def test_products_and_attention_on_two_streams(dq):
+    """Kernels that share SMs, tensor memory and clusters, at once on two streams: the same results
+    as one after the other, and both end."""
+    rng = np.random.default_rng(0)
+    _, _, w = _operand(rng, 4096, 512)
+    _, _, small = _operand(rng, 1024, 256)
+    X, x = _x(rng, 2048, 512, torch.bfloat16), _x(rng, 5, 256, torch.bfloat16)
+    news, lens = [300, 1], [900, 3000]
+    q, cache, table, lt, st, tn = _setup(rng, dq, news, lens, 8, 2, 128, 32, torch.int8)
+    calls = [lambda s: dq.w8a8_linear(X, w, stream=s), lambda s: dq.w8a8_linear(x, small, stream=s),
+             lambda s: dq.paged_attention(q, cache, table, lt, q_starts=st, max_q=300, stream=s),
+             lambda s: dq.paged_attention(q[300:], cache, table[1:], lt[1:], stream=s)]
+    want = [f(None) for f in calls]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for i in range(24):
+        for s, f in ((a, i % 4), (b, (i + 1 + i // 4) % 4)):
+            got.append((f, calls[f](s)))
+    torch.cuda.synchronize()
+    for f, y in got:
+        assert torch.equal(y, want[f])
+
+
+def test_empty_calls(dq):
+    X = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    r = dq.row_quant(X)
+    assert r["codes"].shape == (0, 64) and r["scales"].shape == (0,)
+    w = dict(codes=torch.ones(8, 64, dtype=torch.int8, device="cuda"), scales=torch.ones(8, device="cuda"))
+    assert dq.w8a8_gemm(r, w).shape == (0, 8) and dq.w8a8_linear(X, w).shape == (0, 8)
+    cache = dq.kv_cache(2, 2, 16, 64)
+    kv = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    e64 = torch.empty(0, dtype=torch.int64, device="cuda")
+    assert dq.kv_append(kv, kv, cache, e64) is None
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    assert dq.paged_attention(q, cache, torch.empty(0, 3, **i32), torch.empty(0, **i32)).shape == (0, 4, 64)
+    # two sequences without a token, one without a cache row
+    o = dq.paged_attention(torch.ones(1, 4, 64, dtype=torch.bfloat16, device="cuda"), cache, torch.zeros(3, 0, **i32),
+                           torch.zeros(3, **i32), q_starts=torch.tensor([0, 0, 1, 1], **i32))
+    assert (o == 0).all()
+
+
+def test_helpers_refuse_bad_tensors(dq):
+    dev = dict(device="cuda")
+    X = torch.ones(4, 64, dtype=torch.bfloat16, **dev)
+    w = dict(codes=torch.ones(8, 64, dtype=torch.int8, **dev), scales=torch.ones(8, **dev))
+    for bad in (X.t(), X[0], X.expand(2, 4, 64)):
+        with pytest.raises(ValueError):
+            dq.row_quant(bad)
+    with pytest.raises(dq.DQError):
+        dq.row_quant(X[:1].expand(4, 64))                       # rows on top of one another
+    with pytest.raises(dq.DQError):
+        dq.row_quant(X[:, 1:49])                                # 2-byte aligned
+    with pytest.raises(TypeError):
+        dq.row_quant(X.half())
+    with pytest.raises(ValueError):
+        dq.row_quant(X, torch.ones(63, **dev))
+    with pytest.raises(TypeError):
+        dq.row_quant(X, torch.ones(64, dtype=torch.bfloat16, **dev))
+    with pytest.raises(TypeError):
+        dq.w8a8_linear(X, w, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        dq.w8a8_linear(X[:, :48], w)
+    with pytest.raises(TypeError):
+        dq.w8a8_linear(X, dict(w, codes=w["codes"].to(torch.uint8)))
+    with pytest.raises(ValueError):
+        dq.w8a8_linear(X, dict(w, scales=w["scales"][:7]))
+    with pytest.raises(ValueError):
+        dq.w8a8_linear(X, w, out=torch.empty(4, 9, dtype=torch.bfloat16, **dev))
+    with pytest.raises(ValueError):
+        dq.w8a8_linear(X, w, workspace=torch.empty(8, dtype=torch.uint8, **dev))
+    cache = dq.kv_cache(4, 2, 16, 64)
+    kv = torch.ones(3, 2, 64, dtype=torch.bfloat16, **dev)
+    slots = torch.arange(3, **dev)
+    with pytest.raises(TypeError):
+        dq.kv_append(kv, kv.float(), cache, slots)
+    with pytest.raises(TypeError):
+        dq.kv_append(kv, kv, cache, slots.int())
+    with pytest.raises(ValueError):
+        dq.kv_append(kv, kv[:2], cache, slots)
+    with pytest.raises(ValueError):
+        dq.kv_append(kv, kv, cache, slots, positions=slots.int())
+    with pytest.raises(ValueError):
+        dq.kv_append(kv, kv, cache, slots, q_out=kv)
+    with pytest.raises(ValueError):
+        dq.kv_append(kv, kv, dict(cache, v=cache["v"].transpose(1, 2).contiguous().transpose(1, 2)), slots)
+    with pytest.raises(TypeError):
+        dq.kv_append(kv, kv, dict(cache, v=cache["v"].float()), slots)
+    q = torch.ones(3, 4, 64, dtype=torch.bfloat16, **dev)
+    table, lens = torch.zeros(3, 4, dtype=torch.int32, **dev), torch.ones(3, dtype=torch.int32, **dev)
+    with pytest.raises(TypeError):
+        dq.paged_attention(q.float(), cache, table, lens)
+    with pytest.raises(TypeError):
+        dq.paged_attention(q, cache, table.long(), lens)
+    with pytest.raises(ValueError):
+        dq.paged_attention(q, cache, table[:2], lens[:2])
+    with pytest.raises(ValueError):
+        dq.paged_attention(q, cache, table, lens, max_len=65)
+    with pytest.raises(ValueError):
+        dq.paged_attention(q.transpose(0, 1).contiguous().transpose(0, 1), cache, table, lens)
+    with pytest.raises(dq.DQError):
+        dq.paged_attention(q[:, :3].contiguous(), cache, table, lens)   # 3 heads on 2 key heads
