@@ -458,7 +458,7 @@ Plan8 plan_gemm8(int64_t T, int64_t N, int64_t K) {
       const int64_t slice = per_sm * std::max<int64_t>(4 * std::max(bn / 2, 32 + bn / 4),
                                                        BM * BK / (P.tok_tiles > 2 ? 40 : per_sm == 1 ? 22 : 28) + bn * BK / 40);
       const int64_t toks = std::min<int64_t>(T, bn);
-      const int64_t sum = P.parts > 1 ? 1500 + ceil_div(toks * BM / 4, (int64_t)P.parts * GT) * 600 * per_sm : 10 * bn;
+      const int64_t sum = P.parts > 1 ? 1500 + toks * (BM / 4) * 1200 * per_sm / ((int64_t)P.parts * GT) : 10 * bn;
       const int64_t cost = std::max(waves * (P.per * slice + 4000 + sum), hbm + 4000);
       if (cost < best_cost) {
         best_cost = cost;
