@@ -22,14 +22,14 @@ namespace {
 
 constexpr unsigned FULL = 0xFFFFFFFFu;
 constexpr int WARPS = 4, NT = WARPS * 32;
-constexpr int KG = 16;                            // cache rows of a group
 
 template <int D, bool INT8>
 struct Ring {
+  static constexpr int KG = INT8 ? 32 : 16;       // cache rows of a group: INT8's conversions want the independent work
   static constexpr int RB = D * (INT8 ? 1 : 2);   // bytes of a cache row
   static constexpr int CPR = RB / 16;
   static constexpr int SLOT = 2 * KG * RB + (INT8 ? 2 * KG * 4 : 0);
-  static constexpr int DEPTH = INT8 ? 4 : 3;
+  static constexpr int DEPTH = INT8 && D == 128 ? 2 : 3;
   static constexpr int RING = WARPS * DEPTH * SLOT;
   static constexpr int PITCH = D + 4;             // merge buffer, floats
   static constexpr int MERGE = WARPS * 16 * PITCH * 4 + WARPS * 16 * 8;
@@ -99,6 +99,7 @@ template <int D, bool INT8>
 __global__ void __launch_bounds__(NT, INT8 ? 3 : 2)
 attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
   using R = Ring<D, INT8>;
+  constexpr int KG = R::KG, KH = KG / 16, KN = KG / 8;   // 16-row halves (each within a page), 8-column tiles
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rq = lane >> 2, c = lane & 3;         // fragment row and column group
@@ -187,13 +188,13 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
     }
   }
 
-  // ---- ring of asynchronous copies. A lane's places in a group of 16 rows are fixed: `COPIES` 16-byte
-  // chunks of K and of V, RPC rows apart.
+  // ---- ring of asynchronous copies. A lane's places in 16 rows are fixed: `COPIES` 16-byte chunks of K and
+  // of V, RPC rows apart.
   unsigned char* ring = smem + warp * R::DEPTH * R::SLOT;
   const int groups = ke > kb ? (ke - kb + KG - 1) / KG : 0;
   const int* table = a.page_table + b * a.table_stride;
   const int lg = __ffs(C.page_size) - 1, first_key = kb;
-  constexpr int COPIES = KG * R::CPR / 32, RPC = 32 / R::CPR, ES = INT8 ? 1 : 2;
+  constexpr int COPIES = 16 * R::CPR / 32, RPC = 32 / R::CPR, ES = INT8 ? 1 : 2;
   const int crow = lane / R::CPR, cch = lane % R::CPR;
   const int64_t row_bytes = C.row_stride * ES, page_bytes = C.page_stride * ES;
   const int64_t lane_off = (int64_t)g * C.head_stride * ES + crow * row_bytes + cch * 16;
@@ -206,49 +207,58 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
     kdst[i] = ring_addr + R::k_chunk(crow + i * RPC, cch) * 16;
     vdst[i] = ring_addr + KG * R::RB + R::v_chunk(crow + i * RPC, cch) * 16;
   }
-  auto page_of = [&](int gi) { return gi < groups ? __ldg(table + ((first_key + gi * KG) >> lg)) : 0; };
-  int next_page = page_of(warp);
+  auto page_of = [&](int gi, int h) {
+    const int key = first_key + gi * KG + 16 * h;
+    return gi < groups && key < sq.len ? __ldg(table + (key >> lg)) : 0;
+  };
+  int next_page[KH];
+#pragma unroll
+  for (int h = 0; h < KH; ++h) next_page[h] = page_of(warp, h);
   int issued = warp, slot_w = 0;
   auto issue = [&]() {
     if (issued < groups) {
-      const int key0 = first_key + issued * KG, prow = key0 & (C.page_size - 1);
-      int page = next_page;
-      int live = sq.len - key0;                                      // rows past the length: zeros
-      if ((unsigned)page >= (unsigned)C.pages) {
-        if (lane == 0) atomicOr(A.err_word, ERRBIT_BADARG);
-        page = 0;
-        live = 0;
-      }
-      const int64_t at = page * page_bytes + prow * row_bytes;
-      const char* ks = kbase + at;
-      const char* vs = vbase + at;
       const uint32_t so = slot_w * R::SLOT;
-      if (live >= KG) {
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) {
-          copy16(kdst[i] + so, ks, 16);
-          copy16(vdst[i] + so, vs, 16);
-          ks += RPC * row_bytes;
-          vs += RPC * row_bytes;
+      for (int h = 0; h < KH; ++h) {
+        const int key0 = first_key + issued * KG + 16 * h, prow = key0 & (C.page_size - 1);
+        int page = next_page[h];
+        int live = sq.len - key0;                                    // rows past the length: zeros
+        if ((unsigned)page >= (unsigned)C.pages) {
+          if (lane == 0) atomicOr(A.err_word, ERRBIT_BADARG);
+          page = 0;
+          live = 0;
         }
-      } else {
+        const int64_t at = page * page_bytes + prow * row_bytes;
+        const char* ks = kbase + at;
+        const char* vs = vbase + at;
+        const uint32_t ho = so + 16 * h * R::RB;                     // (the swizzles repeat every 8 rows)
+        if (live >= 16) {
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) {
-          const bool in = crow + i * RPC < live;
-          copy16(kdst[i] + so, in ? ks : static_cast<const char*>(C.k), in ? 16 : 0);
-          copy16(vdst[i] + so, in ? vs : static_cast<const char*>(C.v), in ? 16 : 0);
-          ks += RPC * row_bytes;
-          vs += RPC * row_bytes;
+          for (int i = 0; i < COPIES; ++i) {
+            copy16(kdst[i] + ho, ks, 16);
+            copy16(vdst[i] + ho, vs, 16);
+            ks += RPC * row_bytes;
+            vs += RPC * row_bytes;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < COPIES; ++i) {
+            const bool in = crow + i * RPC < live;
+            copy16(kdst[i] + ho, in ? ks : static_cast<const char*>(C.k), in ? 16 : 0);
+            copy16(vdst[i] + ho, in ? vs : static_cast<const char*>(C.v), in ? 16 : 0);
+            ks += RPC * row_bytes;
+            vs += RPC * row_bytes;
+          }
         }
-      }
-      if (INT8 && lane < 8) {
-        const int part = lane & 3;                                   // four scales
-        const float* src = (lane < 4 ? C.k_scales : C.v_scales) + (((int64_t)page * G + g) << lg) + prow + 4 * part;
-        const int bytes = 4 * max(0, min(4, live - 4 * part));
-        copy16(ring_addr + so + 2 * KG * R::RB + lane * 16, bytes > 0 ? src : C.k_scales, bytes);
+        if (INT8 && lane < 8) {
+          const int part = lane & 3;                                 // four scales
+          const float* src = (lane < 4 ? C.k_scales : C.v_scales) + (((int64_t)page * G + g) << lg) + prow + 4 * part;
+          const int bytes = 4 * max(0, min(4, live - 4 * part));
+          copy16(ring_addr + so + 2 * KG * R::RB + (lane < 4 ? 0 : KG * 4) + 64 * h + part * 16, bytes > 0 ? src : C.k_scales, bytes);
+        }
+        next_page[h] = page_of(issued + WARPS, h);
       }
       issued += WARPS;
-      next_page = page_of(issued);
     }
     slot_w = slot_w + 1 == R::DEPTH ? 0 : slot_w + 1;
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -278,7 +288,7 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
     const uint32_t kp = ring_addr + slot_r * R::SLOT, vp = kp + KG * R::RB;
     slot_r = slot_r + 1 == R::DEPTH ? 0 : slot_r + 1;
     // ---- S = Q K^T (s[t]: rows rq, rq + 8 of columns 8 t + 2c, + 1)
-    float s[2][4] = {};
+    float s[KN][4] = {};
     if constexpr (!INT8) {
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
@@ -289,7 +299,7 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
       }
     } else {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < KN; ++t)
 #pragma unroll
         for (int u = 0; u < D / 64; ++u) {
           const uint4 v = lds16(kp + k_off[u] + t * 8 * R::RB);
@@ -299,25 +309,21 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
         }
     }
     // pairs of a row's scores, in log2 units: x[row][t]
-    float2 x[2][2];
-    float2 vs[2];
-    if constexpr (INT8) {
-      const uint32_t scl = vp + KG * R::RB + 8 * c;
-      const float2 k0 = lds_f2(scl), k1 = lds_f2(scl + 32);
-      vs[0] = lds_f2(scl + 64);
-      vs[1] = lds_f2(scl + 96);
+    float2 x[2][KN];
+    float2 vs[KN];
+#pragma unroll
+    for (int t = 0; t < KN; ++t) {
+      float2 kt = make_float2(1.0f, 1.0f);
+      if constexpr (INT8) {
+        const uint32_t scl = vp + KG * R::RB + 8 * c + 32 * t;
+        kt = lds_f2(scl);
+        vs[t] = lds_f2(scl + KG * 4);
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float2 s2 = make_float2(sc[i], sc[i]);
-        x[i][0] = mul2(mul2(make_float2(s[0][2 * i], s[0][2 * i + 1]), k0), s2);
-        x[i][1] = mul2(mul2(make_float2(s[1][2 * i], s[1][2 * i + 1]), k1), s2);
+        x[i][t] = mul2(make_float2(s[t][2 * i], s[t][2 * i + 1]), make_float2(sc[i], sc[i]));
+        if constexpr (INT8) x[i][t] = mul2(x[i][t], kt);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          x[i][t] = mul2(make_float2(s[t][2 * i], s[t][2 * i + 1]), make_float2(sc[i], sc[i]));
     }
     // ---- mask, running maximum
     const int key0 = first_key + gi * KG;
@@ -325,7 +331,7 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < KN; ++t) {
           if (key0 + 8 * t + 2 * c >= lim[i]) x[i][t].x = -INFINITY;
           if (key0 + 8 * t + 2 * c + 1 >= lim[i]) x[i][t].y = -INFINITY;
         }
@@ -333,14 +339,17 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
     float top[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      top[i] = fmaxf(fmaxf(x[i][0].x, x[i][0].y), fmaxf(x[i][1].x, x[i][1].y));
+      top[i] = fmaxf(x[i][0].x, x[i][0].y);
+#pragma unroll
+      for (int t = 1; t < KN; ++t) top[i] = fmaxf(top[i], fmaxf(x[i][t].x, x[i][t].y));
       top[i] = fmaxf(top[i], __shfl_xor_sync(FULL, top[i], 1));
       top[i] = fmaxf(top[i], __shfl_xor_sync(FULL, top[i], 2));
     }
     bool grow = top[0] > m[0] || top[1] > m[1];
     float vmax = 0.0f;
     if constexpr (INT8) {
-      vmax = fmaxf(fmaxf(vs[0].x, vs[0].y), fmaxf(vs[1].x, vs[1].y));
+#pragma unroll
+      for (int t = 0; t < KN; ++t) vmax = fmaxf(vmax, fmaxf(vs[t].x, vs[t].y));
       grow = grow || (vmax > vunit && vmax < 0x1p126f);
     }
     if (__any_sync(FULL, grow)) {
@@ -368,26 +377,27 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
     }
     // ---- P. bf16 has 8 bits, so a weight goes as two of them (its rounding, and what that leaves): the
     // tensor cores have time to spare, and the result's error is then its own last rounding
-    uint32_t pf[4], pr[4];
+    uint32_t pf[KH][4], pr[KH][4];
     if constexpr (INT8) {
       const float2 v2 = make_float2(vinv, vinv);
-      vs[0] = mul2(vs[0], v2);
-      vs[1] = mul2(vs[1], v2);
+#pragma unroll
+      for (int t = 0; t < KN; ++t) vs[t] = mul2(vs[t], v2);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float mm = m[i] == -INFINITY ? 0.0f : -m[i];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < KN; ++t) {
         float2 p = __fadd2_rn(x[i][t], make_float2(mm, mm));
         p.x = exp2_fast(p.x);
         p.y = exp2_fast(p.y);
         l[i] = __fadd2_rn(l[i], p);      // (the sum takes the weights before their rounding)
         if constexpr (INT8) p = mul2(p, vs[t]);
-        pf[2 * t + i] = pack2<INT8>(p.x, p.y);
+        uint32_t& pk = pf[t / 2][2 * (t & 1) + i];
+        pk = pack2<INT8>(p.x, p.y);
         if constexpr (!INT8) {
-          const float2 hi = bf16x2_to_f2(pf[2 * t + i]);
-          pr[2 * t + i] = pack2<false>(p.x - hi.x, p.y - hi.y);
+          const float2 hi = bf16x2_to_f2(pk);
+          pr[t / 2][2 * (t & 1) + i] = pack2<false>(p.x - hi.x, p.y - hi.y);
         }
       }
     }
@@ -397,35 +407,38 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
       for (int n = 0; n < NTL; n += 2) {
         uint32_t vf[4];
         ldsm4t(vf, vp + R::v_chunk(v_lane, n + (lane >> 4)) * 16);
-        mma16<false>(o[n], pf, vf[0], vf[1]);
-        mma16<false>(o[n + 1], pf, vf[2], vf[3]);
-        mma16<false>(o[n], pr, vf[0], vf[1]);
-        mma16<false>(o[n + 1], pr, vf[2], vf[3]);
+        mma16<false>(o[n], pf[0], vf[0], vf[1]);
+        mma16<false>(o[n + 1], pf[0], vf[2], vf[3]);
+        mma16<false>(o[n], pr[0], vf[0], vf[1]);
+        mma16<false>(o[n + 1], pr[0], vf[2], vf[3]);
       }
     } else {
       // rows 2c, 2c+1, 2c+8, 2c+9 (one swizzle), D/8 codes each from channel (D/8) rq: column n of the
       // product's tile e is channel (D/8) n + e
       constexpr int W = D / 32;
-      uint32_t v[4][W];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t at = kp + v_lane + ((k & 1) + 8 * (k >> 1)) * R::RB;
-        if constexpr (D == 128) {
-          const uint4 y = lds16(at);
-          v[k][0] = y.x; v[k][1] = y.y; v[k][2] = y.z; v[k][3] = y.w;
-        } else {
-          const uint2 y = lds8(at);
-          v[k][0] = y.x; v[k][1] = y.y;
+      for (int h = 0; h < KH; ++h) {
+        uint32_t v[4][W];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t at = kp + v_lane + (16 * h + (k & 1) + 8 * (k >> 1)) * R::RB;
+          if constexpr (D == 128) {
+            const uint4 y = lds16(at);
+            v[k][0] = y.x; v[k][1] = y.y; v[k][2] = y.z; v[k][3] = y.w;
+          } else {
+            const uint2 y = lds8(at);
+            v[k][0] = y.x; v[k][1] = y.y;
+          }
         }
-      }
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140) ^ 0x80808080u, a1 = __byte_perm(v[0][w], v[1][w], 0x7362) ^ 0x80808080u;
-        const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140) ^ 0x80808080u, b1 = __byte_perm(v[2][w], v[3][w], 0x7362) ^ 0x80808080u;
-        mma16<true>(o[4 * w + 0], pf, codes_lo_f16(a0), codes_lo_f16(b0));
-        mma16<true>(o[4 * w + 1], pf, codes_hi_f16(a0), codes_hi_f16(b0));
-        mma16<true>(o[4 * w + 2], pf, codes_lo_f16(a1), codes_lo_f16(b1));
-        mma16<true>(o[4 * w + 3], pf, codes_hi_f16(a1), codes_hi_f16(b1));
+        for (int w = 0; w < W; ++w) {
+          const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140) ^ 0x80808080u, a1 = __byte_perm(v[0][w], v[1][w], 0x7362) ^ 0x80808080u;
+          const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140) ^ 0x80808080u, b1 = __byte_perm(v[2][w], v[3][w], 0x7362) ^ 0x80808080u;
+          mma16<true>(o[4 * w + 0], pf[h], codes_lo_f16(a0), codes_lo_f16(b0));
+          mma16<true>(o[4 * w + 1], pf[h], codes_hi_f16(a0), codes_hi_f16(b0));
+          mma16<true>(o[4 * w + 2], pf[h], codes_lo_f16(a1), codes_lo_f16(b1));
+          mma16<true>(o[4 * w + 3], pf[h], codes_hi_f16(a1), codes_hi_f16(b1));
+        }
       }
     }
     __syncwarp();                        // the slot is free for the next copies
