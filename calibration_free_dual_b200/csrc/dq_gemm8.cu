@@ -478,8 +478,10 @@ Plan8 plan_gemm8(int64_t T, int64_t N, int64_t K) {
 
 cudaError_t launch_cluster(const void* kernel, unsigned x, unsigned y, int smem, int cluster, bool pdl,
                            cudaStream_t s, void** args) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024 &&                           // (what every kernel may have)
+      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+    return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(x, y);
   cfg.blockDim = dim3(GT);

@@ -217,8 +217,10 @@ cudaError_t launch_v(const RowsArgs& A, int nt, cudaStream_t s) {
   constexpr int RD = F32IN && V == 4 ? 2 : 4;
   constexpr auto K = row_quant_kernel<F32IN, V, RD>;
   const int smem = RD * V * nt * CH * (F32IN ? 4 : 2);
-  const cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {                           // (what every kernel may have)
+    const cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
   // as many CTAs as the SMs hold at a time (threads; registers for the wider ones; shared memory)
   const int64_t hold = std::max(1, std::min(2048 / nt / (V == 4 ? 2 : 1), 224 * 1024 / (smem + 1280)));
   K<<<(unsigned)std::min<int64_t>(A.rows, SERVE_SMS * hold), nt, smem, s>>>(A);

@@ -59,6 +59,20 @@ def _scratch(workspace, need: int, like: torch.Tensor) -> torch.Tensor:
     return workspace
 
 
+# The entry points ask for at least 16 bytes of workspace even where the plan of a call uses
+# none; those calls, which neither read nor write them, are given the same 16 bytes.
+_UNUSED_BYTES = 16
+_unused: dict = {}
+
+
+def _unused_scratch(like: torch.Tensor) -> int:
+    t = _unused.get(like.device)
+    if t is None:
+        t = _unused[like.device] = torch.empty((_UNUSED_BYTES,), dtype=torch.uint8,
+                                               device=like.device)
+    return t.data_ptr()
+
+
 def _rows_of(X: torch.Tensor, name: str):
     """(rows, columns, row pitch) of a 2-D row-major tensor. A single row's stride carries no
     meaning and may be anything."""
@@ -143,9 +157,13 @@ def w8a8_gemm(x: dict, w: dict, out_dtype=torch.float32, stream=None,
     if need == 0:
         raise DQError(_lib.DQ_ERR_SHAPE, "K must be a multiple of 16 up to 131072")
     y, code, pitch = _result(out, T, N, out_dtype, xt)
-    sp = _scratch(workspace, need, xt)
-    st = lib.dq_w8a8_gemm(xq, xs, T, wq, ws, N, K, y.data_ptr(), code, pitch, sp.data_ptr(),
-                          sp.numel(), _raw_stream(dev))
+    if workspace is None and need <= _UNUSED_BYTES:
+        sp = _unused_scratch(xt)
+    else:
+        workspace = _scratch(workspace, need, xt)
+        sp = workspace.data_ptr()
+    st = lib.dq_w8a8_gemm(xq, xs, T, wq, ws, N, K, y.data_ptr(), code, pitch, sp, need,
+                          _raw_stream(dev))
     if st:
         _check(st, "dq_w8a8_gemm")
     return y
@@ -204,11 +222,16 @@ def _cache_of(cache: dict, dev: int) -> _lib.dq_kv_cache:
     k, v = cache["k"], cache["v"]
     _need_cuda(k, "cache k")
     dtype = k.dtype
-    if dtype not in CACHE_TYPES:
-        raise TypeError("the cache must be bfloat16 or int8, got %s" % dtype)
-    _expect(k, dev, "cache k", dtype)
-    _expect(v, dev, "cache v", dtype)
     shape, strides = k.shape, k.stride()
+    if dtype is torch.int8:
+        kind = _lib.DQ_CACHE_INT8
+    elif dtype is torch.bfloat16:
+        kind = _lib.DQ_CACHE_BF16
+    else:
+        raise TypeError("the cache must be bfloat16 or int8, got %s" % dtype)
+    if k.get_device() != dev:
+        _expect(k, dev, "cache k", dtype)
+    _expect(v, dev, "cache v", dtype)
     if len(shape) != 4 or v.shape != shape or v.stride() != strides or strides[3] != 1:
         raise ValueError("cache k and v must be [pages, kv_heads, page_size, head_dim] with the "
                          "same strides and contiguous channels")
@@ -219,17 +242,17 @@ def _cache_of(cache: dict, dev: int) -> _lib.dq_kv_cache:
         ps = G * S * D
     if G == 1:
         hs = S * D
-    if dtype is torch.bfloat16:
-        return _lib.dq_kv_cache(_lib.DQ_CACHE_BF16, S, D, G, P, k.data_ptr(), v.data_ptr(), ps,
-                                hs, rs, None, None)
+    if kind == _lib.DQ_CACHE_BF16:
+        return _lib.dq_kv_cache(kind, S, D, G, P, k.data_ptr(), v.data_ptr(), ps, hs, rs, None,
+                                None)
     ks, vs = cache["k_scales"], cache["v_scales"]
-    for t, name in ((ks, "cache k_scales"), (vs, "cache v_scales")):
-        if (not isinstance(t, torch.Tensor) or t.dtype is not torch.float32
-                or t.get_device() != dev or t.shape != shape[:3] or not t.is_contiguous()):
-            _expect(t, dev, name, torch.float32)
-            raise ValueError(name + " must be contiguous [pages, kv_heads, page_size]")
-    return _lib.dq_kv_cache(_lib.DQ_CACHE_INT8, S, D, G, P, k.data_ptr(), v.data_ptr(), ps, hs,
-                            rs, ks.data_ptr(), vs.data_ptr())
+    _expect(ks, dev, "cache k_scales", torch.float32)
+    _expect(vs, dev, "cache v_scales", torch.float32)
+    rows = (P, G, S)
+    if ks.shape != rows or vs.shape != rows or not (ks.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("cache scales must be contiguous [pages, kv_heads, page_size]")
+    return _lib.dq_kv_cache(kind, S, D, G, P, k.data_ptr(), v.data_ptr(), ps, hs, rs,
+                            ks.data_ptr(), vs.data_ptr())
 
 
 def _heads(x: torch.Tensor, dev: int, name: str, dtype, T: int, H: int, D: int) -> int:
@@ -349,11 +372,15 @@ def paged_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor,
     a = _lib.dq_attention(q.data_ptr(), out.data_ptr(), qs, os, T, B, H, 1 if causal else 0, sp,
                           lp, page_table.data_ptr(), pitch, max_q, max_len,
                           D ** -0.5 if scale is None else scale)
-    lib = _lib.get()
+    call = _lib.get().dq_paged_attention
     cr, ar = ctypes.byref(c), ctypes.byref(a)
-    need = lib.dq_paged_attention_workspace_bytes(cr, ar)
-    ws = _scratch(workspace, need if need > 16 else 16, q)
-    st = lib.dq_paged_attention(cr, ar, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    st = _lib.DQ_ERR_WORKSPACE
+    if workspace is None:
+        st = call(cr, ar, _unused_scratch(q), _UNUSED_BYTES, _raw_stream(dev))
+    if st == _lib.DQ_ERR_WORKSPACE:                # split sequences need room for their parts
+        need = _lib.get().dq_paged_attention_workspace_bytes(cr, ar)
+        workspace = _scratch(workspace, need, q)
+        st = call(cr, ar, workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
     if st:
         _check(st, "dq_paged_attention")
     return out
