@@ -181,26 +181,24 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   const dq_kv_cache& C = A.cache;
   const int G = C.kv_heads, group = A.group;
   // the last row tiles (which see the most cache rows) go first
-  const int64_t idx = blockIdx.x;
-  const int split = (int)(idx % P.splits);
-  const int g = (int)(idx / P.splits % G);
-  const int64_t rt = P.row_tiles - 1 - idx / P.splits / G;
-  const int b = blockIdx.y;
+  const unsigned splits = (unsigned)P.splits, above = blockIdx.x / splits;
+  const int split = (int)(blockIdx.x - above * splits), g = (int)(above % (unsigned)G);
+  const int rt = (int)P.row_tiles - 1 - (int)(above / (unsigned)G), b = blockIdx.y;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const SeqBounds sq = seq_bounds(a, b);
-  if (sq.bad && idx == 0 && tid == 0) atomicOr(A.err_word, ERRBIT_BADARG);
-  const int64_t rows = (int64_t)sq.n * group, row0 = rt * 256;
+  if (sq.bad && blockIdx.x == 0 && tid == 0) atomicOr(A.err_word, ERRBIT_BADARG);
+  const int rows = sq.n * group, row0 = rt * 256;    // (rows of a sequence stay below 2^31)
   if (row0 >= rows) return;
-  const int64_t kb = split * P.chunk;
+  const int kb = split * (int)P.chunk;
   if (split > 0 && kb >= sq.len) return;
   // tiles of cache rows that the two row tiles see
   int nt[2];
-  const int64_t chunk_end = min64(sq.len, kb + P.chunk);
+  const int chunk_end = min(sq.len, kb + (int)P.chunk);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int64_t first = row0 + 128 * t, last = min64(first + 127, rows - 1);
-    const int64_t ke = first < rows ? min64(chunk_end, visible(a, sq, (int)(last / group))) : 0;
-    nt[t] = ke > kb ? (int)((ke - kb + KT - 1) / KT) : 0;
+    const int first = row0 + 128 * t, last = min(first + 127, rows - 1);
+    const int ke = first < rows ? min(chunk_end, visible(a, sq, last / group)) : 0;
+    nt[t] = ke > kb ? (ke - kb + KT - 1) / KT : 0;
   }
   const int n = max(nt[0], nt[1]);
 
@@ -239,14 +237,14 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const bool tail = kb + (int64_t)n * KT > sq.len;     // the last tile reaches past the sequence
+  const bool tail = kb + n * KT > sq.len;     // the last tile reaches past the sequence
 
   if (warp < 8) {
     more_registers<T::R_SOFTMAX>();
     // ================================================================= softmax, one thread a row
     const int t = warp >> 2, sp = warp & 3;
     const int r = sp * 32 + lane;
-    const int64_t row = row0 + 128 * t + r;
+    const int row = row0 + 128 * t + r;
     const bool there = row < rows;
     // ---- queries of the row tile: 16-byte chunks, a row by D/8 threads
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // (the exponent's factor is positive)
@@ -254,16 +252,21 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     {
       constexpr int CPR = D / 8;
       const int ch = lane % CPR;
-#pragma unroll 4
-      for (int i = 0; i < 32 / (32 / CPR); ++i) {
-        const int qr = sp * 32 + i * (32 / CPR) + lane / CPR;
-        const int64_t qrow = row0 + 128 * t + qr;
-        uint4 v = make_uint4(0, 0, 0, 0);
+      constexpr int ROUNDS = CPR;                   // 32 / CPR rows a round
+      uint4 in[ROUNDS];
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {             // all loads in flight
+        const int qrow = row0 + 128 * t + sp * 32 + i * (32 / CPR) + lane / CPR;
+        in[i] = make_uint4(0, 0, 0, 0);
         if (qrow < rows) {
-          const int64_t tok = sq.start + qrow / group;
-          const int h = g * group + (int)(qrow % group);
-          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_stride + (int64_t)h * D) + ch);
+          const int tok = qrow / group, h = g * group + (qrow - tok * group);
+          in[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (sq.start + tok) * a.q_stride + (int64_t)h * D) + ch);
         }
+      }
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {
+        const int qr = sp * 32 + i * (32 / CPR) + lane / CPR;
+        const uint4 v = in[i];
         uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
         if constexpr (INT8) {
           float mx = 0.0f;
@@ -288,7 +291,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       if (lane == 0) mbar_arrive(qready);
     }
     // cache rows this row sees, from the CTA's first on
-    const int lim = there ? (int)(min64(chunk_end, visible(a, sq, (int)(row / group))) - kb) : 0;
+    const int lim = there ? min(chunk_end, visible(a, sq, row / group)) - kb : 0;
     const bool warp_there = row0 + 128 * t + sp * 32 < rows;
     float c = fabsf(a.scale) * 1.4426950408889634f;
     if (INT8) c /= qfac[128 * t + r];
@@ -416,8 +419,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     if (ok && nt[t] > 0) ok = mbar_wait(ofull0 + 8 * t, 0) && !*fail;
     if (ok && warp_there) {
       tc_fence_after();
-      const int64_t tok = sq.start + (there ? row / group : 0);
-      const int h = g * group + (int)(there ? row % group : 0);
+      const int tok_of = there ? row / group : 0, h = g * group + (there ? row - tok_of * group : 0);
+      const int64_t tok = sq.start + tok_of;
       const bool none = lim <= 0;              // no cache row to see here
       const float inv = none ? 0.0f : 1.0f / l;
       const int64_t at = ((int64_t)split * a.tokens + tok) * a.heads + h;
@@ -525,14 +528,14 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const int lg = __ffs(C.page_size) - 1, lbox = lg < 7 ? lg : 7, box = 1 << lbox;
     const int* table = a.page_table + b * a.table_stride;
     auto page_of = [&](int j) {                      // -1: no row of the sequence
-      const int key = (int)kb + j * KT + (lane << lbox);
+      const int key = kb + j * KT + (lane << lbox);
       return (lane << lbox) < KT && j < n && key < sq.len ? __ldg(table + (key >> lg)) : -1;
     };
-    auto in_tile = [&](int j) { return min(KT >> lbox, (sq.len - (int)kb - j * KT + box - 1) >> lbox); };
+    auto in_tile = [&](int j) { return min(KT >> lbox, (sq.len - kb - j * KT + box - 1) >> lbox); };
     bool ok = true;
     int i = 0, next = page_of(0);
     for (int j = 0; j < n && ok; ++j) {
-      const int live = in_tile(j), prow = ((int)kb + j * KT + (lane << lbox)) & (C.page_size - 1);
+      const int live = in_tile(j), prow = (kb + j * KT + (lane << lbox)) & (C.page_size - 1);
       int page = next;
       next = page_of(j + 1);
       if (lane < live && (page < 0 || page >= C.pages)) {
@@ -568,7 +571,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     if (!INT8 && ok && tail && n > 0) {
       const int slot = (i - 1) % RING;
       if (mbar_wait_warp(rfull + 8 * slot, (uint32_t)((i - 1) / RING) & 1u)) {
-        const int valid = sq.len - (int)kb - (n - 1) * KT;
+        const int valid = sq.len - kb - (n - 1) * KT;
         for (int e = valid * 8 + lane; e < KT * 8; e += 32)
           for (int h = 0; h < D / 64; ++h)
             *reinterpret_cast<uint4*>(base + T::KV_OFF + slot * T::TILE + h * T::HALF + e * 16) = make_uint4(0, 0, 0, 0);
@@ -593,7 +596,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const int* table = a.page_table + b * a.table_stride;
     float nks = 0.0f, nvs = 0.0f;
     auto fetch_scales = [&](int j) {                 // of row w of tile j; 0 past the sequence
-      const int key = (int)kb + j * KT + w;
+      const int key = kb + j * KT + w;
       nks = nvs = 0.0f;
       if (j >= n || key >= sq.len) return;
       const int page = __ldg(table + (key >> lg));
@@ -609,7 +612,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       ok = mbar_wait(rawfull0 + 8 * rslot, (uint32_t)(i / T::RAW_SLOTS) & 1u);
       ok = ok && mbar_wait(empty0 + 8 * slot, ((uint32_t)(i / SLOTS) & 1u) ^ 1u);
       if (!ok) break;
-      const int valid = sq.len - (int)kb - j * KT;   // rows past them may be anything: zeros
+      const int valid = sq.len - kb - j * KT;   // rows past them may be anything: zeros
       const uint4* src = reinterpret_cast<const uint4*>(base + T::RAW_OFF + rslot * T::RAW);
       unsigned char* tile = base + T::KV_OFF + slot * T::TILE + (ch >> 2) * T::HALF;
 #pragma unroll

@@ -79,7 +79,7 @@ dq_status check_attention(const dq_kv_cache* c, const dq_attention* a, int* grou
   *group = a->heads / c->kv_heads;
   if (*group > 128) return DQ_ERR_UNSUPPORTED;
   if (a->tokens > INT32_MAX / 2 || a->sequences > 65535 || a->max_len > INT32_MAX / 2 ||
-      a->max_q > a->tokens)
+      a->max_q > a->tokens || a->max_q * *group > INT32_MAX / 2)
     return DQ_ERR_SHAPE;
   return DQ_OK;
 }
