@@ -252,15 +252,22 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     {
       constexpr int CPR = D / 8;
       const int ch = lane % CPR;
-      constexpr int ROUNDS = CPR;                   // 32 / CPR rows a round
+      constexpr int ROUNDS = CPR, RPR = 32 / CPR;   // rows a round
       uint4 in[ROUNDS];
+      // (token, head) of this lane's rows, RPR rows apart, without a division each
+      const int q0 = row0 + 128 * t + sp * 32 + lane / CPR, up = RPR / group, over = RPR - up * group;
+      int tok = q0 / group, hh = q0 - tok * group;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (sq.start + tok) * a.q_stride + (int64_t)(g * group + hh) * D + ch * 8;
+      const int64_t step = up * a.q_stride + over * D, wrap = a.q_stride - group * D;
 #pragma unroll
       for (int i = 0; i < ROUNDS; ++i) {             // all loads in flight
-        const int qrow = row0 + 128 * t + sp * 32 + i * (32 / CPR) + lane / CPR;
         in[i] = make_uint4(0, 0, 0, 0);
-        if (qrow < rows) {
-          const int tok = qrow / group, h = g * group + (qrow - tok * group);
-          in[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (sq.start + tok) * a.q_stride + (int64_t)h * D) + ch);
+        if (q0 + i * RPR < rows) in[i] = __ldg(reinterpret_cast<const uint4*>(src));
+        src += step;
+        hh += over;
+        if (hh >= group) {
+          hh -= group;
+          src += wrap;
         }
       }
 #pragma unroll
@@ -425,31 +432,30 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       const float inv = none ? 0.0f : 1.0f / l;
       const int64_t at = ((int64_t)split * a.tokens + tok) * a.heads + h;
       if (P.splits > 1 && there) P.part_ml[at] = none ? make_float2(-INFINITY, 0.0f) : make_float2(ref, l);
-#pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t o[32];
-        if (nt[t] > 0) {
-          tmem_ld32_async(o_addr + 32 * q, o);
-          tmem_wait_ld();
+      uint32_t o[D];
+      if (nt[t] > 0) {
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) tmem_ld32_async(o_addr + 32 * q, o + 32 * q);
+        tmem_wait_ld();
+      }
+      if (none) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) o[i] = 0u;
+      }
+      if (there && P.splits == 1) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + (int64_t)h * D);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack16<false>(f_of(o[8 * i + 2 * e]) * inv, f_of(o[8 * i + 2 * e + 1]) * inv);
+          dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (none) {
+      } else if (there) {
+        uint4* dst = reinterpret_cast<uint4*>(P.part_o + at * D);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0u;
-        }
-        if (!there) continue;
-        if (P.splits == 1) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + (int64_t)h * D + 32 * q);
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            w[i] = pack16<false>(f_of(o[2 * i]) * inv, f_of(o[2 * i + 1]) * inv);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(P.part_o + at * D + 32 * q);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        }
+        for (int i = 0; i < D / 4; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
       tc_fence_before();
     }
