@@ -24,7 +24,6 @@ cudaError_t launch_attention_tiles(const AttnArgs& A, const AttnPlan& P, cudaStr
 
 namespace {
 
-__device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;

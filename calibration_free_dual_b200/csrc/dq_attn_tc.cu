@@ -14,7 +14,9 @@
 //   * 9: pages by TMA, K and V in turn: bf16 with the 128-byte swizzle straight to a ring of four tiles;
 //   * INT8 cache, 12-15: codes from a ring of their own, exactly to fp16, to the ring of tiles; per-row
 //     scales beside them. Keys' scales multiply the scores, values' scales the weights; the weights are kept
-//     relative to a running power of two above the values' scales (fp16's range).
+//     relative to a running power of two above the values' scales (fp16's range). Every softmax thread
+//     reads all scales of a tile, 64 16-byte reads that load/store units return in 4 clocks each: with
+//     the conversion's about 3300 clocks a tile pair, where the products take 2048; this bounds the INT8 path.
 // Long sequences are split over CTAs when the row tiles do not fill the SMs (dq_attn.cu joins).
 // Every wait is bounded; on timeout the kernel raises the error word, frees its TMEM and returns.
 #include <algorithm>
@@ -27,14 +29,14 @@ namespace dq {
 namespace {
 
 constexpr unsigned FULL = 0xFFFFFFFFu;
+constexpr int R_CONVERT = 88;                     // registers a thread of the converting warps (INT8: 184 + 56 + 88 a set)
 constexpr int KT = 128;                           // cache rows of a tile
 
 template <int D, bool INT8>
 struct Tc {
   static constexpr int NT = INT8 ? 512 : 384;
-  // registers a thread, of the launch's (65536 / NT): softmax warps, products and TMA, conversion
+  // registers a thread, of the launch's (65536 / NT): softmax warps (two sets of four), products and TMA
   static constexpr int R_SOFTMAX = INT8 ? 184 : 208, R_PRODUCT = INT8 ? 56 : 88;
-  static constexpr int R_CONVERT = 88;
   static constexpr int SLOTS = INT8 ? 3 : 4;      // K and V tiles in shared memory
   static constexpr int RAW_SLOTS = INT8 ? 3 : 0;  // tiles of codes on their way to them
   static constexpr int HALF = KT * 128;           // [128 rows][64 channels] of 2 bytes, swizzled
@@ -596,7 +598,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         mbar_wait(rfull + 8 * (k % RING), (uint32_t)(k / RING) & 1u);
     }
   } else if constexpr (INT8) {
-    fewer_registers<T::R_CONVERT>();
+    fewer_registers<R_CONVERT>();
     // ================================================================= codes to fp16
     constexpr int CPR = D / 16, RPP = 128 / CPR, ROUNDS = KT / RPP;   // 16 codes per thread and round
     const int w = tid - 12 * 32, ch = w % CPR, r0 = w / CPR;
