@@ -156,6 +156,13 @@ __device__ __forceinline__ float2 exp2_poly(float2 y) {
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
+// s += the two bf16 of a word
+__device__ __forceinline__ void add_bf16x2(float2& s, uint32_t w) {
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "add.rn.f32.bf16 %0, lo, %0;\n\tadd.rn.f32.bf16 %1, hi, %1;\n\t}"
+      : "+f"(s.x), "+f"(s.y) : "r"(w));
+}
+
 template <int N> struct Int { static constexpr int value = N; };
 
 template <int N> __device__ __forceinline__ void more_registers() {
@@ -397,15 +404,21 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                 y0.x = exp2_fast(y0.x); y0.y = exp2_fast(y0.y);
               }
               y1.x = exp2_fast(y1.x); y1.y = exp2_fast(y1.y);
-              l0 = __fadd2_rn(l0, y0);
-              l1 = __fadd2_rn(l1, y1);
               if constexpr (INT8) {
+                l0 = __fadd2_rn(l0, y0);
+                l1 = __fadd2_rn(l1, y1);
                 const float4 v4 = *reinterpret_cast<const float4*>(vs + i);
                 y0 = mul2(y0, make_float2(v4.x, v4.y));
                 y1 = mul2(y1, make_float2(v4.z, v4.w));
               }
               p[(i - i0) / 2] = pack16<INT8>(y0.x, y0.y);
               p[(i - i0) / 2 + 1] = pack16<INT8>(y1.x, y1.y);
+              if constexpr (!INT8) {
+                // the sum takes the weights as the product does: a row with one large weight is then
+                // not scaled by that weight's rounding
+                add_bf16x2(l0, p[(i - i0) / 2]);
+                add_bf16x2(l1, p[(i - i0) / 2 + 1]);
+              }
             }
             tmem_st16_async(s_addr + i0 / 2, p);
           }
