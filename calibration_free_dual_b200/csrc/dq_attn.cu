@@ -533,23 +533,49 @@ attn_join_kernel(const AttnArgs A, const AttnPlan P) {
   if ((int)i >= sq.n) return;
   const int chunk = (int)P.chunk, splits = sq.len == 0 ? 1 : (sq.len + chunk - 1) / chunk;
   const int64_t at0 = (sq.start + i) * a.heads + h, pitch = a.tokens * a.heads;
+  constexpr int CH = D / 32, AHEAD = 8;            // channels of a lane; parts in flight
+  // every lane looks at the parts lane, lane + 32, ...
   float mx = -INFINITY;
-  for (int s = 0; s < splits; ++s) mx = fmaxf(mx, P.part_ml[s * pitch + at0].x);
-  float x[D / 32] = {}, sum = 0.0f;
-  for (int s = 0; s < splits; ++s) {
-    const float2 ml = P.part_ml[s * pitch + at0];
-    if (ml.x == -INFINITY) continue;
-    const float f = exp2_fast(ml.x - mx);
-    sum += ml.y * f;
-    const float* src = P.part_o + (s * pitch + at0) * D + lane * (D / 32);
-    if constexpr (D == 128) {
-      const float4 y = *reinterpret_cast<const float4*>(src);
-      x[0] += y.x * f; x[1] += y.y * f; x[2] += y.z * f; x[3] += y.w * f;
-    } else {
-      const float2 y = *reinterpret_cast<const float2*>(src);
-      x[0] += y.x * f; x[1] += y.y * f;
+  for (int s = lane; s < splits; s += 32) mx = fmaxf(mx, P.part_ml[s * pitch + at0].x);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
+  float x[CH] = {}, sum = 0.0f;
+  for (int s0 = 0; s0 < splits; s0 += 32) {
+    const int cnt = min(32, splits - s0);
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (lane < cnt) ml = P.part_ml[(s0 + lane) * pitch + at0];
+    // a part without a visible row (-1) adds nothing; one whose factor is 0 still hands on a NaN
+    const float f = ml.x == -INFINITY ? -1.0f : exp2_fast(ml.x - mx);
+    if (!(f < 0.0f)) sum += ml.y * f;
+    for (int k = 0; k < cnt; k += AHEAD) {
+      float y[AHEAD][CH];
+#pragma unroll
+      for (int e = 0; e < AHEAD; ++e) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) y[e][j] = 0.0f;
+        if (k + e < cnt) {
+          const float* src = P.part_o + ((s0 + k + e) * pitch + at0) * D + lane * CH;
+          if constexpr (D == 128) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            y[e][0] = v.x; y[e][1] = v.y; y[e][2] = v.z; y[e][3] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            y[e][0] = v.x; y[e][1] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < AHEAD; ++e) {
+        const float fe = __shfl_sync(FULL, f, min(k + e, 31));
+        if (k + e < cnt && !(fe < 0.0f)) {
+#pragma unroll
+          for (int j = 0; j < CH; ++j) x[j] += y[e][j] * fe;
+        }
+      }
     }
   }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(FULL, sum, off);
   const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (sq.start + i) * a.out_stride + (int64_t)h * D + lane * (D / 32);
 #pragma unroll

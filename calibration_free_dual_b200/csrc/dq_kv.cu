@@ -76,18 +76,20 @@ kv_append_kernel(const AppendArgs A) {
   // first ones ahead of the token's slot and position too.
   constexpr int UNR = 4;
   struct { Raw4<F32IN> lo, hi; } x8[UNR];
+  const char* kp = static_cast<const char*>(A.k) + t * A.k_stride * ES;
+  const char* vp = static_cast<const char*>(A.v) + t * A.v_stride * ES;
+  const char* qp = static_cast<const char*>(A.q) + t * A.q_stride * ES;
+  const int lane_row = threadIdx.x / TPR;
   auto load_rounds = [&](int first) {
 #pragma unroll
     for (int u = 0; u < UNR; ++u) {
-      const int r = first + u * RPP + threadIdx.x / TPR;
+      const int r = first + u * RPP + lane_row;
       const bool is_q = r >= 2 * G, is_v = !is_q && r >= G;
-      const int h = is_q ? r - 2 * G : is_v ? r - G : r;
+      const int h = r - (is_q ? 2 * G : is_v ? G : 0);
       const int lo = is_v ? 8 * sub : lo_r, hi = is_v ? 8 * sub + 4 : hi_r;
       x8[u] = {};
       if (r < rows) {
-        const char* src = is_q ? static_cast<const char*>(A.q) + (t * A.q_stride + (int64_t)h * D) * ES
-                          : is_v ? static_cast<const char*>(A.v) + (t * A.v_stride + (int64_t)h * D) * ES
-                                 : static_cast<const char*>(A.k) + (t * A.k_stride + (int64_t)h * D) * ES;
+        const char* src = (is_q ? qp : is_v ? vp : kp) + h * (D * ES);
         x8[u].lo = load4<F32IN>(src + lo * ES);
         x8[u].hi = load4<F32IN>(src + hi * ES);
       }
@@ -112,6 +114,10 @@ kv_append_kernel(const AppendArgs A) {
   }
   const int lg = __ffs(C.page_size) - 1;
   const int64_t page = slot < 0 ? 0 : slot >> lg, prow = slot < 0 ? 0 : slot & (C.page_size - 1);
+  const int64_t at = (page * C.page_stride + prow * C.row_stride) * (INT8 ? 1 : 2);
+  char* kdst = static_cast<char*>(C.k) + at;
+  char* vdst = static_cast<char*>(C.v) + at;
+  char* qo = static_cast<char*>(A.q_out) + t * A.q_out_stride * 2;
   bool bad = false;
   // (whole warps run the same count of rounds)
   for (int first = 0; first < rows; first += UNR * RPP) {
@@ -119,10 +125,19 @@ kv_append_kernel(const AppendArgs A) {
 #pragma unroll
     for (int u = 0; u < UNR; ++u) {
       if (first + u * RPP >= rows) break;
-      const int r = first + u * RPP + threadIdx.x / TPR;
+      const int r = first + u * RPP + lane_row;
       const bool is_q = r >= 2 * G, is_v = !is_q && r >= G;
       const bool live = r < rows && (is_q || slot >= 0);
-      const int h = is_q ? r - 2 * G : is_v ? r - G : r;
+      const int h = r - (is_q ? 2 * G : is_v ? G : 0);
+      // a value goes to a bf16 cache as it came
+      if (!INT8 && !F32IN && is_v) {
+        if (live) {
+          char* dst = vdst + h * C.head_stride * 2;
+          *reinterpret_cast<uint2*>(dst + 16 * sub) = make_uint2(x8[u].lo.u[0], x8[u].lo.u[1]);
+          *reinterpret_cast<uint2*>(dst + 16 * sub + 8) = make_uint2(x8[u].hi.u[0], x8[u].hi.u[1]);
+        }
+        continue;
+      }
       const int lo = is_v ? 8 * sub : lo_r, hi = is_v ? 8 * sub + 4 : hi_r;
       float x[8];
       unpack4<F32IN>(x8[u].lo, x);
@@ -136,7 +151,7 @@ kv_append_kernel(const AppendArgs A) {
           for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
         }
       }
-      const int64_t at = page * C.page_stride + (int64_t)h * C.head_stride + prow * C.row_stride;
+      char* cdst = (is_v ? vdst : kdst) + h * C.head_stride * (INT8 ? 1 : 2);
       if (INT8 && __any_sync(FULL, live && !is_q)) {
         uint32_t a = 0;
 #pragma unroll
@@ -160,15 +175,13 @@ kv_append_kernel(const AppendArgs A) {
           uint32_t w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
           uint32_t w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
           if (inf) w0 = w1 = 0u;
-          int8_t* dst = static_cast<int8_t*>(is_v ? C.v : C.k) + at;
-          *reinterpret_cast<uint32_t*>(dst + lo) = w0;
-          *reinterpret_cast<uint32_t*>(dst + hi) = w1;
-          if (sub == 0) (is_v ? C.v_scales : C.k_scales)[(page * G + h) * C.page_size + prow] = d;
+          *reinterpret_cast<uint32_t*>(cdst + lo) = w0;
+          *reinterpret_cast<uint32_t*>(cdst + hi) = w1;
+          if (sub == 0) (is_v ? C.v_scales : C.k_scales)[((page * G + h) << lg) + prow] = d;
         }
       }
       if (live && (!INT8 || is_q)) {
-        char* dst = is_q ? static_cast<char*>(A.q_out) + (t * A.q_out_stride + (int64_t)h * D) * 2
-                         : static_cast<char*>(is_v ? C.v : C.k) + at * 2;
+        char* dst = is_q ? qo + h * (D * 2) : cdst;
         *reinterpret_cast<uint2*>(dst + lo * 2) = pack4(x);
         *reinterpret_cast<uint2*>(dst + hi * 2) = pack4(x + 4);
       }
