@@ -518,19 +518,20 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
     P.part_ml[((int64_t)split * a.tokens + t) * a.heads + h] = make_float2(mx, sum);
 }
 
-// Joins the splits: one warp per (token, head) row
-template <int D>
+// Joins the splits: `W` warps per (token, head) row, each with eight parts in flight; a warp takes parts
+// 8 w .. 8 w + 7 of every 8 W
+template <int D, int W>
 __global__ void __launch_bounds__(128)
 attn_join_kernel(const AttnArgs A, const AttnPlan P) {
   // (launched while the parts are still at work)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const dq_attention& a = A.a;
-  const int lane = threadIdx.x & 31;
-  const unsigned row = blockIdx.x * 4 + threadIdx.x / 32;
+  const int lane = threadIdx.x & 31, w = threadIdx.x / 32 % W;
+  const unsigned row = blockIdx.x * (4 / W) + threadIdx.x / (32 * W);
   const int b = blockIdx.y;
   const SeqBounds sq = seq_bounds(a, b);
   const unsigned i = row / (unsigned)a.heads, h = row - i * a.heads;
-  if ((int)i >= sq.n) return;
+  if ((int)i >= sq.n) return;                      // (W = 4: the whole CTA)
   const int chunk = (int)P.chunk, splits = sq.len == 0 ? 1 : (sq.len + chunk - 1) / chunk;
   const int64_t at0 = (sq.start + i) * a.heads + h, pitch = a.tokens * a.heads;
   constexpr int CH = D / 32, AHEAD = 8;            // channels of a lane; parts in flight
@@ -547,7 +548,7 @@ attn_join_kernel(const AttnArgs A, const AttnPlan P) {
     // a part without a visible row (-1) adds nothing; one whose factor is 0 still hands on a NaN
     const float f = ml.x == -INFINITY ? -1.0f : exp2_fast(ml.x - mx);
     if (!(f < 0.0f)) sum += ml.y * f;
-    for (int k = 0; k < cnt; k += AHEAD) {
+    for (int k = AHEAD * w; k < cnt; k += AHEAD * W) {
       float y[AHEAD][CH];
 #pragma unroll
       for (int e = 0; e < AHEAD; ++e) {
@@ -576,6 +577,20 @@ attn_join_kernel(const AttnArgs A, const AttnPlan P) {
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(FULL, sum, off);
+  if constexpr (W > 1) {
+    __shared__ float other[W - 1][D];
+    if (w > 0) {
+#pragma unroll
+      for (int j = 0; j < CH; ++j) other[w - 1][j * 32 + lane] = x[j];
+    }
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int u = 0; u < W - 1; ++u) {
+#pragma unroll
+      for (int j = 0; j < CH; ++j) x[j] += other[u][j * 32 + lane];
+    }
+  }
   const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (sq.start + i) * a.out_stride + (int64_t)h * D + lane * (D / 32);
 #pragma unroll
@@ -594,7 +609,9 @@ AttnPlan plan_attention(const AttnArgs& A, void* ws) {
   const int64_t base = std::max<int64_t>(1, P.row_tiles * A.cache.kv_heads * a.sequences);
   if (P.tile == 16) {
     // about twelve CTAs an SM in all where the sequences are long: lengths differ, and many small
-    // CTAs even out; none with less than 768 cache rows (what a CTA spends besides takes as long as about 200)
+    // CTAs even out; none with less than 768 cache rows (what a CTA spends besides takes as long as about
+    // 200). INT8, 16000 rows: 48 sequences 216 us (six CTAs an SM 229, three 263), 16 92 (100, 99); 2 sequences
+    // of 60000 69 us (67, 61)
     const int64_t want = (12 * SERVE_SMS + base - 1) / base;
     P.chunk = std::max<int64_t>(768, ((a.max_len + want - 1) / want + 63) / 64 * 64);
   } else {
@@ -624,9 +641,12 @@ AttnPlan plan_attention(const AttnArgs& A, void* ws) {
 
 template <int D>
 cudaError_t launch_join(const AttnArgs& A, const AttnPlan& P, cudaStream_t s) {
+  // a row's parts are read in turns of eight a warp: four warps from nine parts on (79 parts, 64 rows: the
+  // whole call 87 -> 69 us; 22 parts 77 -> 72)
+  const bool wide = P.splits > 8;
   const int64_t rows = A.a.max_q * A.a.heads;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((rows + 3) / 4), (unsigned)A.a.sequences);
+  cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 3) / 4), (unsigned)A.a.sequences);
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -634,7 +654,8 @@ cudaError_t launch_join(const AttnArgs& A, const AttnPlan& P, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, A, P);
+  const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, attn_join_kernel<D, 4>, A, P)
+                             : cudaLaunchKernelEx(&cfg, attn_join_kernel<D, 1>, A, P);
   count_launches(1);
   return e;
 }
