@@ -13,6 +13,7 @@
 #include "dq.h"
 #include "dq_internal.h"
 #include "dq_gemm.h"
+#include "dq_serve.h"
 
 namespace {
 

@@ -29,7 +29,6 @@ enum Scale : int { SCALE_BF16 = 0, SCALE_E8M0 = 1, SCALE_E4M3 = 2 };
 constexpr unsigned ERRBIT_NONFINITE = 1u;
 constexpr unsigned ERRBIT_TIMEOUT = 2u;
 constexpr unsigned ERRBIT_BADWARM = 4u;
-constexpr unsigned ERRBIT_BADARG = 4u;    // an index or length on the device out of its range
 
 constexpr float NVFP4_TENSOR_DIV = 2688.0f;   // 6 (E2M1 max) * 448 (E4M3 max)
 

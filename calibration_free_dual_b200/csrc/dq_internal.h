@@ -104,9 +104,6 @@ inline int fmt_block(int kind, int group) {
 inline int fmt_scale_bytes(int kind) { return (kind == 0 || kind == 4) ? 2 : 1; }   // bf16: 2
 inline int fmt_elem_bits(int kind) { return kind >= 4 ? 8 : 4; }
 
-// per-device error word (dq_api.cu); false when the device or the symbol cannot be had
-bool error_word(unsigned** out);
-
 // measurement hooks (dq_api.cu)
 void count_launches(int n);
 void timing_before(cudaStream_t s);

@@ -11,6 +11,10 @@
 namespace dq {
 
 constexpr int SERVE_SMS = 148;          // SMs of the part the launches are planned for
+constexpr unsigned ERRBIT_BADARG = 4u;  // error word: an index or length on the device out of its range
+
+// per-device error word (dq_api.cu); false when the device or the symbol cannot be had
+bool error_word(unsigned** out);
 
 struct RowsArgs {
   const void* X;

@@ -415,7 +415,8 @@ DQ_API dq_status dq_decode(const void* codes, int64_t count, int32_t codec, floa
                            void* stream);
 
 /* Synchronises `stream`, then returns and clears the device error word of the current
- * device: DQ_ERR_NONFINITE, DQ_ERR_TIMEOUT or DQ_OK (DQ_ERR_CUDA if a CUDA call fails). */
+ * device: DQ_ERR_NONFINITE, DQ_ERR_TIMEOUT, DQ_ERR_INVALID_ARG (an index, length or warm start on the device
+ * out of its range) or DQ_OK (DQ_ERR_CUDA if a CUDA call fails). */
 DQ_API dq_status dq_last_device_error(void* stream);
 
 /* Measurement hooks (no computation). dq_set_timing_events: before the i-th launch of the
