@@ -6,7 +6,9 @@
 // units) and adds P V to the output in registers: one pass over the cache, no scores in memory. The
 // four warps of a CTA take groups of 16 cache rows in turn, each through its own ring of asynchronous
 // copies (no barrier in the loop), and merge at the end; long sequences are split over CTAs
-// (`chunk` cache rows each) whose partial results a second kernel joins. The bound is the cache's bytes.
+// (`chunk` cache rows each) whose partial results a second kernel joins. The bound is the cache's bytes: 48 sequences of 16000 rows, 8 heads
+// of 128: bf16 299 us, 6.7 TB/s (the copy rate is 6.5); INT8 215 us, 4.8 TB/s, there bound by the issue
+// slots of the conversion (53%) and the latency around it.
 //
 // INT8 cache: codes become fp16 exactly (an exponent byte beside each code and one subtraction), the keys'
 // scales multiply the scores, the values' scales the weights before their rounding to fp16. The

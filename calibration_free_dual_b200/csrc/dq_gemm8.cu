@@ -13,6 +13,9 @@
 //   * split: for few tiles (few tokens, or a small weight). One CTA per 128 weight rows x 32 to 256 tokens
 //     and all or part of K; the parts of a tile form a cluster and add their int32 sums through distributed
 //     shared memory (exact, so the split does not show in the result).
+// Bounds, measured (bf16 output, alone, uniform codes): many tiles are bound by the tensor pipe (75% busy) and by how
+// fast L2 feeds it: T = 8192, N x K = 14336 x 4096 321 us (3.0e15 op/s), 4096 x 14336 307 us (3.1e15). Few tokens by
+// the weight's bytes: T = 1, 14336 x 4096 15.2 us (3.9 TB/s in one short wave), 4096 x 4096 7.0 us.
 // Every wait on an mbarrier is bounded; on timeout the kernel raises the error word, frees its TMEM
 // and returns.
 #include <algorithm>

@@ -50,7 +50,8 @@ def _x(rng, T, n, dtype, pad=0):
 @pytest.mark.parametrize("T,n,pad,with_c", [(1, 16, 0, False), (3, 80, 16, True),
                                             (700, 1280, 0, True), (5, 4096, 8, True),
                                             (333, 4112, 0, False), (2, 14336, 0, True),
-                                            (600, 11008, 0, True), (3, 20000, 32, True)])
+                                            (600, 11008, 0, True), (3, 20000, 32, True),
+                                            (500, 16400, 16, True), (7, 32768, 0, False), (3, 32784, 0, True)])
 def test_row_quant_bit_exact(dq, dtype, T, n, pad, with_c):
     rng = np.random.default_rng(T + n)
     X = _x(rng, T, n, dtype, pad)
