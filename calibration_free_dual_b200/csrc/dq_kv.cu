@@ -5,9 +5,9 @@
 // threads, each with 8 channels in registers: with the half-split rotation four of the first
 // half and their four partners (no exchange between lanes), otherwise 8 in a row. A CTA takes one
 // token's rows of all heads, so the token's cos and sin are loaded once a thread. The INT8
-// row maximum is reduced by shuffles among the row's threads. 6001 tokens, 32 + 32 + 32 heads of 128, bf16: 54 us,
-// 298 MB at 5.5 TB/s (reads and writes mixed); 32 + 8 + 8 heads, INT8 cache: 41 us, 3.4 TB/s (the quantization's
-// instructions); 64 tokens 3.1 us.
+// row maximum is reduced by shuffles among the row's threads. 6001 tokens, 32 + 32 + 32 heads of 128, bf16: 52 us,
+// 298 MB at 5.7 TB/s (reads and writes mixed); 32 + 8 + 8 heads, INT8 cache: 31 us, 4.5 TB/s (instructions and latency);
+// 64 tokens 2.7 us.
 #include <algorithm>
 
 #include "dq_device.cuh"
@@ -18,7 +18,6 @@ namespace dq {
 namespace {
 
 constexpr unsigned FULL = 0xFFFFFFFFu;
-constexpr int KV_NT = 256;
 
 // four channels: as they lie in memory, and as binary32
 template <bool F32IN>
@@ -59,11 +58,11 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   a = x;
 }
 
-template <int D, bool INT8, bool F32IN>
-__global__ void __launch_bounds__(KV_NT)
+template <int D, bool INT8, bool F32IN, int NT>
+__global__ void __launch_bounds__(NT, NT == 64 ? 12 : 1)
 kv_append_kernel(const AppendArgs A) {
   constexpr int TPR = D / 8;                        // threads of one head's row
-  constexpr int RPP = KV_NT / TPR;                  // rows at a time
+  constexpr int RPP = NT / TPR;                     // rows at a time
   constexpr int ES = F32IN ? 4 : 2;
   const int64_t t = blockIdx.x;
   const int sub = threadIdx.x % TPR;
@@ -76,7 +75,7 @@ kv_append_kernel(const AppendArgs A) {
   const int hi_r = halves && turned ? A.rot.dim / 2 + 4 * sub : 8 * sub + 4;
   // rows of the token: keys, values, queries. The loads of UNR rounds go ahead of their stores, the
   // first ones ahead of the token's slot and position too.
-  constexpr int UNR = 4;
+  constexpr int UNR = NT == 64 ? 6 : 4;
   struct { Raw4<F32IN> lo, hi; } x8[UNR];
   const char* kp = static_cast<const char*>(A.k) + t * A.k_stride * ES;
   const char* vp = static_cast<const char*>(A.v) + t * A.v_stride * ES;
@@ -192,18 +191,25 @@ kv_append_kernel(const AppendArgs A) {
   if (bad) atomicOr(A.err_word, ERRBIT_NONFINITE);
 }
 
-template <int D>
-cudaError_t launch_dim(const AppendArgs& A, int esize, cudaStream_t s) {
+template <int D, bool INT8, bool F32IN>
+cudaError_t launch_typed(const AppendArgs& A, cudaStream_t s) {
   const unsigned g = (unsigned)A.tokens;
-  if (A.cache.kind == DQ_CACHE_INT8) {
-    if (esize == 4) kv_append_kernel<D, true, true><<<g, KV_NT, 0, s>>>(A);
-    else kv_append_kernel<D, true, false><<<g, KV_NT, 0, s>>>(A);
-  } else {
-    if (esize == 4) kv_append_kernel<D, false, true><<<g, KV_NT, 0, s>>>(A);
-    else kv_append_kernel<D, false, false><<<g, KV_NT, 0, s>>>(A);
-  }
+  // Many tokens: 64 threads each, six rounds of loads ahead, so that more tokens are in flight and few threads idle in
+  // the last round (6001 tokens, INT8, 32 + 8 + 8 heads: 31 us, with 256 threads 41). Few tokens: 256 threads, for
+  // latency (64 tokens of that kind: 2.7 us, with 64 threads 5.0; even at about 600: 6.2 and 6.3), unless
+  // 64 threads are done in two rounds anyway (600 tokens, 8 + 2 + 2 heads of 64: 2.9 us, with 256 threads 4.8).
+  const bool narrow = A.tokens > 4 * SERVE_SMS || (A.q_heads + 2 * (int64_t)A.cache.kv_heads) * (D / 8) <= 2 * 64;
+  if (narrow) kv_append_kernel<D, INT8, F32IN, 64><<<g, 64, 0, s>>>(A);
+  else kv_append_kernel<D, INT8, F32IN, 256><<<g, 256, 0, s>>>(A);
   count_launches(1);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_dim(const AppendArgs& A, int esize, cudaStream_t s) {
+  if (A.cache.kind == DQ_CACHE_INT8)
+    return esize == 4 ? launch_typed<D, true, true>(A, s) : launch_typed<D, true, false>(A, s);
+  return esize == 4 ? launch_typed<D, false, true>(A, s) : launch_typed<D, false, false>(A, s);
 }
 
 }  // namespace

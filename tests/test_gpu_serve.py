@@ -217,7 +217,8 @@ def _random_cache(rng, dq, pages, G, S, D, dtype, layout="head"):
                          [(1, 1, 1, 64, 16, 64, False, "head"), (5, 8, 2, 128, 16, 128, False, "token"),
                           (64, 32, 8, 128, 32, 64, False, "pair"), (77, 7, 1, 64, 64, 64, True, "head"),
                           (33, 12, 3, 128, 256, 24, True, "token"), (9, 4, 4, 64, 128, 0, False, "head"),
-                          (200, 0, 5, 128, 16, 8, False, "head")])
+                          (200, 0, 5, 128, 16, 8, False, "head"), (700, 26, 6, 128, 32, 96, False, "token"),
+                          (593, 7, 3, 64, 64, 32, True, "pair"), (20, 50, 2, 64, 16, 64, False, "head")])
 def test_append_bit_exact(dq, dtype, kind, T, H, G, D, S, dim, inter, layout):
     rng = np.random.default_rng(T + H + G)
     pages = -(-T // S) + 3
@@ -257,17 +258,19 @@ def test_append_bit_exact(dq, dtype, kind, T, H, G, D, S, dim, inter, layout):
         assert torch.equal(got.cpu(), torch.from_numpy(qr).to(torch.float32).to(torch.bfloat16))
 
 
-def test_append_rotates_queries_in_place(dq):
+@pytest.mark.parametrize("T,H", [(11, 6), (11, 30), (650, 40)])
+def test_append_rotates_queries_in_place(dq, T, H):
     rng = np.random.default_rng(1)
-    T, H, G, D = 11, 6, 2, 64
+    G, D = 2, 64
     qkv = torch.from_numpy(rng.standard_normal((T, (H + 2 * G) * D)).astype(np.float32)).to(torch.bfloat16).cuda()
     q, k, v = (qkv[:, a * D:b * D].view(T, b - a, D) for a, b in ((0, H), (H, H + G), (H + G, H + 2 * G)))
     cos, sin = _tables(rng, 30, D)
     rot = dict(cos=torch.from_numpy(cos).cuda(), sin=torch.from_numpy(sin).cuda(),
-               positions=torch.arange(T, dtype=torch.int32, device="cuda"))
+               positions=torch.arange(T, dtype=torch.int32, device="cuda") % 30)
     slots = torch.arange(T, device="cuda")
-    a = dq.kv_append(k, v, dq.kv_cache(1, G, 16, D), slots, q=q, **rot)
-    b = dq.kv_append(k, v, dq.kv_cache(1, G, 16, D), slots, q=q, q_out=q, **rot)
+    pages = -(-T // 16)
+    a = dq.kv_append(k, v, dq.kv_cache(pages, G, 16, D), slots, q=q, **rot)
+    b = dq.kv_append(k, v, dq.kv_cache(pages, G, 16, D), slots, q=q, q_out=q, **rot)
     assert b.data_ptr() == q.data_ptr() and torch.equal(a, b)
 
 
