@@ -108,18 +108,20 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
   const dq_attention& a = A.a;
   const dq_kv_cache& C = A.cache;
   const int G = C.kv_heads, group = A.group;
-  // (at most 16 rows a key head: one row tile)
-  const unsigned splits = (unsigned)P.splits;
-  const int g = (int)(blockIdx.x / splits), split = (int)(blockIdx.x - g * splits);
+  // row tiles that read the same cache rows are neighbours, so that one of them finds the rows in L2
+  const unsigned splits = (unsigned)P.splits, above = blockIdx.x / (unsigned)P.row_tiles;
+  const int g = (int)(above / splits), split = (int)(above - g * splits);
+  const int r0 = 16 * (int)(blockIdx.x - above * (unsigned)P.row_tiles);
   const int b = blockIdx.y;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const SeqBounds sq = seq_bounds(a, b);
   if (sq.bad && blockIdx.x == 0 && tid == 0) atomicOr(A.err_word, ERRBIT_BADARG);
-  const int rows = sq.n * group;
-  if (rows == 0) return;
+  const int rows = min(16, sq.n * group - r0);     // of this tile
+  if (rows <= 0) return;
+  const int first = r0 / group, last = (r0 + rows - 1) / group;   // its tokens
   const int kb = split * (int)P.chunk;
   if (split > 0 && kb >= sq.len) return;
-  const int ke = min(min(sq.len, kb + (int)P.chunk), visible(a, sq, sq.n - 1));
+  const int ke = min(min(sq.len, kb + (int)P.chunk), visible(a, sq, last));
 
   // this thread's two rows: query pointer, visible cache rows
   const __nv_bfloat16* qp[2];
@@ -129,14 +131,14 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
   for (int i = 0; i < 2; ++i) {
     const int r = rq + 8 * i;
     there[i] = r < rows;
-    const int t = there[i] ? r / group : 0;
+    const int t = there[i] ? (r0 + r) / group : 0;
     lim[i] = there[i] ? visible(a, sq, t) : 0;
-    const int h = g * group + (there[i] ? r - t * group : 0);
+    const int h = g * group + (there[i] ? r0 + r - t * group : 0);
     qp[i] = static_cast<const __nv_bfloat16*>(a.q) + (sq.start + t) * a.q_stride + (int64_t)h * D;
   }
   // rows that every row of the tile sees need no mask
   // (a row that is not there needs none either: nothing of it is kept)
-  const int unmasked = min(ke, visible(a, sq, 0));
+  const int unmasked = min(ke, visible(a, sq, first));
 #pragma unroll
   for (int i = 0; i < 2; ++i) lim[i] = min(lim[i], ke);
 
@@ -494,8 +496,8 @@ attn_rows_kernel(const AttnArgs A, const AttnPlan P) {
     const float2 x = ml[w * 16 + r];
     sum += x.x == -INFINITY ? 0.0f : x.y * exp2_fast(x.x - mx);
   }
-  const int64_t t = sq.start + r / group;
-  const int h = g * group + r % group;
+  const int64_t t = sq.start + (r0 + r) / group;
+  const int h = g * group + (r0 + r) % group;
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) {
     const int d = 32 * j + 4 * e;
@@ -600,13 +602,15 @@ attn_join_kernel(const AttnArgs A, const AttnPlan P) {
     *reinterpret_cast<uint32_t*>(dst + j) = pack2<false>(x[j] * inv, x[j + 1] * inv);
 }
 
-// Few (token, head) rows a key head: 16-row tiles, bound by the cache's bytes; more: 256-row tiles on
-// the tensor cores. Sequences are split where the row tiles do not fill the SMs.
+// Few (token, head) rows a key head: 16-row tiles, bound by the cache's bytes, up to three of them on an INT8
+// cache; more: 256-row tiles on the tensor cores, whose time hardly depends on how many rows of a tile there are (48
+// sequences of 16000 rows, 8 heads of 128, in us with tiles of 16 and of 256: bf16 4 rows 301 and 452, 16 308 and
+// 454, 32 426 and 395; INT8 4 rows 216 and 647, 20 415 and 650, 48 607 and 663, 64 786 and 600). Sequences are split where the row tiles do not fill the SMs.
 AttnPlan plan_attention(const AttnArgs& A, void* ws) {
   AttnPlan P = {};
   const dq_attention& a = A.a;
   const int64_t rows = a.max_q * A.group;
-  P.tile = rows <= 16 ? 16 : 256;
+  P.tile = rows <= (A.cache.kind == DQ_CACHE_INT8 ? 48 : 16) ? 16 : 256;
   P.row_tiles = (rows + P.tile - 1) / P.tile;
   const int64_t base = std::max<int64_t>(1, P.row_tiles * A.cache.kv_heads * a.sequences);
   if (P.tile == 16) {
@@ -668,7 +672,7 @@ cudaError_t launch_kind(const AttnArgs& A, const AttnPlan& P, cudaStream_t s) {
   constexpr auto K = attn_rows_kernel<D, INT8>;
   cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, R::SMEM);
   if (e != cudaSuccess) return e;
-  const int64_t x = P.splits * A.cache.kv_heads;
+  const int64_t x = P.splits * A.cache.kv_heads * P.row_tiles;
   if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
   K<<<dim3((unsigned)x, (unsigned)A.a.sequences), NT, R::SMEM, s>>>(A, P);
   count_launches(1);

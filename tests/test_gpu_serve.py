@@ -405,7 +405,7 @@ def test_attention_page_sizes_and_layouts(dq, kind, S, layout, n):
 
 
 @pytest.mark.parametrize("kind", [torch.bfloat16, torch.int8])
-@pytest.mark.parametrize("news,lens", [([4, 2], [9, 300]), ([150, 3], [77, 500])])
+@pytest.mark.parametrize("news,lens", [([4, 2], [9, 300]), ([12, 5], [9, 1300]), ([150, 3], [77, 500])])
 def test_attention_not_causal(dq, kind, news, lens):
     rng = np.random.default_rng(9)
     q, cache, table, lt, st, tn = _setup(rng, dq, news, lens, 8, 2, 64, 16, kind)
@@ -415,7 +415,7 @@ def test_attention_not_causal(dq, kind, news, lens):
 
 
 @pytest.mark.parametrize("kind", [torch.bfloat16, torch.int8])
-@pytest.mark.parametrize("n", [1, 5, 150])
+@pytest.mark.parametrize("n", [1, 5, 22, 150])
 def test_attention_rows_without_keys_are_zero(dq, kind, n):
     """More new tokens than cache rows: the first see nothing; an empty sequence gives zeros."""
     rng = np.random.default_rng(n)
